@@ -1,6 +1,6 @@
-"""B200 (sm_100a) masked attention: forward, backward and e4m3 forward.
+"""B200 (sm_100a) masked attention: forward, backward, e4m3 forward and an 8-bit paged K/V cache.
 
-Thin Python binding over the C ABI declared in ``include/attn.h``: every function
+Thin Python binding over the C ABI declared in ``include/attn.h`` and ``include/attn_kv8.h``: every function
 here only marshals arguments (torch tensors supply device memory and streams);
 all of the computation happens in ``libattn_b200.so``. Importing succeeds without a
 GPU; calls that need one fail with a RuntimeError. If the library has not been
@@ -19,6 +19,9 @@ Typical use (q [total_q, hq, d], k / v [total_k, hkv, d] bf16 CUDA tensors)::
 
     attn_fp8_transpose_v(plan, v8, vt8, ldv)         # e4m3 inputs (uint8 tensors)
     attn_masked_fwd_fp8(plan, q8, k8, vt8, ldv, q_scale, k_scale, v_scale, out, lse)
+
+The 8-bit paged cache (page tables on the GPU, append, attention for a few query tokens,
+page selection, gather) is bound in ``kv8``; its names are available here too.
 
 ``kv_splits`` (split-KV) and ``q_rows`` (a query-row shard, see ``sharding``) are
 further attn_plan() arguments; attn_plan_dry_run() gives the plan statistics without
@@ -42,12 +45,14 @@ MASK_KIND = {"FULL": 0, "CAUSAL": 1, "SLIDING_WINDOW": 2, "PREFIX_LM": 3, "CHUNK
              "CUSTOM": 6, "BLOCK_SPARSE": 7}
 RANGE_FULL, RANGE_CAUSAL, RANGE_INV_CAUSAL, RANGE_BI_CAUSAL, RANGE_CHUNK_CAUSAL = 0, 1, 2, 3, 4
 
-# every symbol include/attn.h declares
+# every symbol the headers in include/ declare
 EXPORTS = ("attn_plan", "attn_masked_fwd", "attn_plan_get_tile_classes", "attn_plan_get_stats",
            "attn_plan_check_status", "attn_plan_set_debug", "attn_plan_destroy", "attn_classify_host",
            "attn_status_string", "attn_masked_fwd_noalloc", "attn_test_exp2_poly", "attn_plan_dry_run",
            "attn_plan_bwd", "attn_masked_bwd", "attn_masked_fwd_fp8", "attn_fp8_transpose_v",
-           "attn_test_transpose_mask_tile", "attn_test_noalloc_debug", "attn_plan_bwd_dry_run")
+           "attn_test_transpose_mask_tile", "attn_test_noalloc_debug", "attn_plan_bwd_dry_run",
+           "attn_page_tables", "attn_kv8_append", "attn_kv8_gather", "attn_kv8_plan", "attn_kv8_plan_destroy",
+           "attn_kv8_fwd", "attn_kv8_select")
 
 
 class AttnError(RuntimeError):
@@ -133,6 +138,13 @@ def lib() -> ctypes.CDLL:
         L.attn_masked_fwd_noalloc.argtypes = [ctypes.POINTER(attn_problem_t), ctypes.POINTER(attn_mask_desc_t),
                                               vp, vp, vp, vp, vp, vp]
         L.attn_test_noalloc_debug.argtypes = [i32, i64]
+        L.attn_page_tables.argtypes = [vp, vp]
+        L.attn_kv8_append.argtypes = [vp, vp, i64, vp, i64, vp, i32, vp]
+        L.attn_kv8_gather.argtypes = [vp, vp, i32, vp, i32, i64, vp, vp, vp]
+        L.attn_kv8_plan.argtypes = [vp, ctypes.POINTER(vp)]
+        L.attn_kv8_plan_destroy.argtypes = [vp]
+        L.attn_kv8_fwd.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp]
+        L.attn_kv8_select.argtypes = [vp, vp, vp, i32, i32, vp, vp, i32, vp]
         for n in EXPORTS:
             if n != "attn_status_string":
                 getattr(L, n).restype = i32
@@ -559,3 +571,7 @@ def attn_test_transpose_mask_tile(tile_words: np.ndarray) -> np.ndarray:
     dst = np.zeros(512, dtype=np.uint32)
     _check(lib().attn_test_transpose_mask_tile(src.ctypes.data, dst.ctypes.data), "attn_test_transpose_mask_tile")
     return dst
+
+
+from .kv8 import (Kv8Cache, Kv8Plan, attn_kv8_append, attn_kv8_fwd, attn_kv8_gather,  # noqa: E402
+                  attn_kv8_plan, attn_kv8_plan_destroy, attn_kv8_select, attn_page_tables, forward_kv8)

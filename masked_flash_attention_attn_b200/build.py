@@ -19,7 +19,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libattn_b200.so")
-SOURCES = ["attn_plan.cpp", "attn_custom.cu", "attn_fwd.cu", "attn_bwd.cu"]
+SOURCES = ["attn_plan.cpp", "attn_custom.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_kv8.cu", "attn_kv8_fwd.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -1,0 +1,736 @@
+// The 8-bit paged K/V cache around its attention (attn_kv8_fwd.cu): page tables and slot maps
+// from request lengths, quantising append, gather to bf16, and page selection.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "kv8_common.cuh"
+
+namespace kv8 {
+namespace {
+
+// ---- page tables and slot maps ------------------------------------------------------------------
+// Every CTA scans the request lengths itself (two int32 per request, from L2 after the first
+// CTA), keeps the three prefix sums -- new tokens, pages taken, pages given back -- in shared
+// memory and then writes its share of the tokens, table entries and ring entries, each found by a
+// binary search in the prefixes. So one launch does it all without a grid-wide wait: nothing
+// that a CTA reads is written in the call (table entries below the old page count and the ring's
+// occupied part are read, entries from the old page count on and the ring's empty part written).
+struct Sums { long long tok; int take, give; };
+
+__device__ __forceinline__ int pages_of(int n, int shift) { return int((unsigned(n) + (1u << shift) - 1) >> shift); }
+
+__device__ __forceinline__ Sums add(Sums a, Sums b) { return Sums{a.tok + b.tok, a.take + b.take, a.give + b.give}; }
+__device__ __forceinline__ Sums up(Sums a, int o) {
+  return Sums{__shfl_up_sync(~0u, a.tok, o), __shfl_up_sync(~0u, a.take, o), __shfl_up_sync(~0u, a.give, o)};
+}
+
+// the largest i in [0, n) with a[i] <= x (a non-decreasing, a[0] = 0 <= x)
+__device__ __forceinline__ int find(const int* a, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (a[m] <= x) lo = m; else hi = m;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(1024) page_tables_kernel(attn_page_tables_t a, int shift) {
+  extern __shared__ int s_prefix[];
+  const int B = a.batch;
+  int* s_tok = s_prefix;
+  int* s_take = s_tok + B + 1;
+  int* s_give = s_take + B + 1;
+  __shared__ Sums s_warp[32];
+  __shared__ Sums s_total;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
+  const int cap = int(min((long long)(a.max_pages_per_seq) << shift, 0x7fffffffLL));
+  const int n = a.num_pages;
+  int head = a.free_state[0] % n;
+  head = head < 0 ? head + n : head;
+  const int count = min(max(a.free_state[1], 0), n);
+
+  auto request = [&](int b, int& old_n, int& new_n) -> bool {
+    old_n = min(max(a.old_lens[b], 0), cap);
+    new_n = a.new_lens[b];
+    const bool valid = new_n >= 0 && new_n <= cap;
+    if (!valid) new_n = old_n;
+    return valid;
+  };
+  auto sums = [&](int old_n, int new_n) {
+    const int d = pages_of(new_n, shift) - pages_of(old_n, shift);
+    return Sums{new_n > old_n ? new_n - old_n : 0, max(d, 0), max(-d, 0)};
+  };
+
+  const int per = (B + nt - 1) / nt, b0 = min(B, tid * per), b1 = min(B, b0 + per);
+  Sums mine{0, 0, 0};
+  int bad = 0;
+  for (int b = b0; b < b1; ++b) {
+    int o, w;
+    bad |= !request(b, o, w);
+    mine = add(mine, sums(o, w));
+  }
+  Sums inc = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const Sums x = up(inc, o);
+    if (lane >= o) inc = add(inc, x);
+  }
+  if (lane == 31) s_warp[warp] = inc;
+  bad = __syncthreads_or(bad);
+  if (warp == 0) {
+    Sums w = lane < nw ? s_warp[lane] : Sums{0, 0, 0};
+    Sums wi = w;
+    for (int o = 1; o < 32; o <<= 1) {
+      const Sums x = up(wi, o);
+      if (lane >= o) wi = add(wi, x);
+    }
+    if (lane == 31) s_total = wi;
+    s_warp[lane] = Sums{wi.tok - w.tok, wi.take - w.take, wi.give - w.give};
+  }
+  __syncthreads();
+  Sums total = s_total;
+  const int status = bad ? 2 : total.tok > a.max_tokens ? 3 : total.take > count ? 1 : 0;
+  const int missing = status == 1 ? total.take - count : 0;
+  const bool ok = status == 0;
+  if (!ok) total.tok = 0, total.take = 0;
+  Sums at = s_warp[warp];
+  at = Sums{at.tok + inc.tok - mine.tok, at.take + inc.take - mine.take, at.give + inc.give - mine.give};
+  for (int b = b0; b < b1; ++b) {
+    int o, w;
+    request(b, o, w);
+    s_tok[b] = ok ? int(at.tok) : 0;
+    s_take[b] = ok ? at.take : 0;
+    s_give[b] = at.give;
+    at = add(at, sums(o, w));
+  }
+  if (tid == 0) {
+    s_tok[B] = int(total.tok);
+    s_take[B] = total.take;
+    s_give[B] = total.give;
+  }
+  __syncthreads();
+
+  const int g0 = blockIdx.x * nt + tid, gn = gridDim.x * nt;
+  auto ring = [&](int i) {        // head + i modulo the ring, 0 <= i <= 2 n
+    unsigned x = unsigned(head) + unsigned(i);
+    return x % unsigned(n);
+  };
+  for (int b = g0; b <= B; b += gn) {
+    a.cu_seqlens_q[b] = s_tok[b];
+    if (b < B) {
+      int o, w;
+      request(b, o, w);
+      a.kv_lens[b] = ok || w < o ? w : o;
+    }
+  }
+  if (g0 == 0) {
+    a.next_state[0] = int(ring(total.take));
+    a.next_state[1] = count - total.take + total.give;
+    a.next_state[2] = status;
+    a.next_state[3] = missing;
+  }
+  for (int t = g0; t < a.max_tokens; t += gn) {
+    int slot = -1, pos = -1;
+    if (t < int(total.tok)) {
+      const int b = find(s_tok, B, t);
+      int o, w;
+      request(b, o, w);
+      pos = o + t - s_tok[b];
+      const int pi = pos >> shift, before = pages_of(o, shift);
+      const int pg = pi < before ? a.page_table[int64_t(b) * a.max_pages_per_seq + pi]
+                                 : a.free_pages[ring(s_take[b] + pi - before)];
+      if (unsigned(pg) < unsigned(n)) slot = (pg << shift) + (pos & ((1 << shift) - 1));
+    }
+    a.slots[t] = slot;
+    if (a.positions) a.positions[t] = pos;
+  }
+  for (int j = g0; j < total.take; j += gn) {
+    const int b = find(s_take, B, j);
+    int o, w;
+    request(b, o, w);
+    a.page_table[int64_t(b) * a.max_pages_per_seq + pages_of(o, shift) + j - s_take[b]] = a.free_pages[ring(j)];
+  }
+  for (int j = g0; j < total.give; j += gn) {
+    const int b = find(s_give, B, j);
+    int o, w;
+    request(b, o, w);
+    a.free_pages[ring(count + j % n)] = a.page_table[int64_t(b) * a.max_pages_per_seq + pages_of(w, shift) + j - s_give[b]];
+  }
+}
+
+// ---- append ---------------------------------------------------------------------------------------
+// One CTA takes the runs (tokens of one page that follow one another) that start among its `span` tokens, for
+// one head and K or V. A run's new values stay in registers between the maximum and the
+// rounding, so they are read once; a page block's codes are contiguous. HBM-bound: 2 bytes in and 1
+// out per value. Power-of-two scales lose nothing with a floating 8-bit format (the
+// relative step is the same at every exponent) and make requantising after a growth exact
+// but for subnormal codes, so a page filled token by token holds what one call would write.
+struct AppendArgs {
+  const __nv_bfloat16* x[2];
+  int64_t stride[2];
+  uint8_t* codes[2];
+  float* scale[2];
+  int8_t* bounds;
+  const int32_t* slots;
+  int32_t tokens, span, hkv, d, shift, num_slots;
+};
+
+template <int NT, int NV>
+__global__ void __launch_bounds__(NT) append_kernel(AppendArgs a) {
+  __shared__ int s_list[128];
+  __shared__ int s_count, s_stop, s_taken[NT / 32];
+  __shared__ int2 s_run[128];     // token and place of the run's tokens
+  __shared__ unsigned s_max[NT / 32];
+  __shared__ int s_hi[256], s_lo[256];
+  const int tid = threadIdx.x, h = blockIdx.y;
+  const bool is_v = blockIdx.z != 0;
+  const __nv_bfloat16* src = is_v ? a.x[1] : a.x[0];
+  const int64_t stride = is_v ? a.stride[1] : a.stride[0];
+  const int t0 = blockIdx.x * a.span, ps = 1 << a.shift, D = a.d, vd = D >> 3;
+  const int vshift = 31 - __clz(vd);
+  if (tid == 0) s_count = 0;
+  __syncthreads();
+  if (tid < a.span && t0 + tid < a.tokens) {
+    const int t = t0 + tid, s = a.slots[t];
+    if (unsigned(s) < unsigned(a.num_slots)) {
+      int j = t - 1;              // a run starts where the token before (skipped ones aside) is of another page
+      while (j >= 0 && unsigned(a.slots[j]) >= unsigned(a.num_slots)) --j;
+      if (j < 0 || (a.slots[j] >> a.shift) != (s >> a.shift)) s_list[atomicAdd(&s_count, 1)] = t;
+    }
+  }
+  __syncthreads();
+  const int runs = s_count;
+  for (int r = 0; r < runs; ++r) {
+    const int t = s_list[r], pg = a.slots[t] >> a.shift, off = a.slots[t] & (ps - 1);
+    const bool bound = !is_v && a.bounds != nullptr;
+    if (bound)
+      for (int c = tid; c < D; c += NT) s_hi[c] = -128, s_lo[c] = 127;
+    // the run's tokens, in order: those of the page up to the first of another page
+    int n = 0;
+    for (int w0 = t;; w0 += NT) {
+      if (tid == 0) s_stop = NT;
+      __syncthreads();
+      const int w = w0 + tid, s = w < a.tokens ? a.slots[w] : -1;
+      const bool in = unsigned(s) < unsigned(a.num_slots);
+      if (w >= a.tokens || (in && (s >> a.shift) != pg)) atomicMin(&s_stop, tid);
+      __syncthreads();
+      const int stop = s_stop;
+      const bool take = in && tid < stop;
+      const unsigned m = __ballot_sync(~0u, take);
+      if ((tid & 31) == 0) s_taken[tid >> 5] = __popc(m);
+      __syncthreads();
+      int at = n + __popc(m & ((1u << (tid & 31)) - 1u));
+      for (int i = 0; i < NT / 32; ++i) {
+        if (i < (tid >> 5)) at += s_taken[i];
+        n += s_taken[i];
+      }
+      if (take && at < ps) s_run[at] = make_int2(w, s & (ps - 1));
+      if (stop < NT || n >= ps) break;
+    }
+    n = min(n, ps);
+    __syncthreads();
+    const int vecs = n << vshift;
+
+    uint4 x[NV];
+    unsigned top = 0;             // the largest finite |x|, as bf16 bits
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = tid + i * NT;
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (v < vecs)
+        x[i] = *reinterpret_cast<const uint4*>(src + int64_t(s_run[v >> vshift].x) * stride + h * D + (v & (vd - 1)) * 8);
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const unsigned lo = w[j] & 0x7fffu, hi = (w[j] >> 16) & 0x7fffu;
+        if (lo < 0x7f80u) top = max(top, lo);
+        if (hi < 0x7f80u) top = max(top, hi);
+      }
+    }
+    top = __reduce_max_sync(~0u, top);
+    if ((tid & 31) == 0) s_max[tid >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) top = max(top, s_max[i]);
+
+    const int64_t block = int64_t(pg) * a.hkv + h;
+    float* scale = (is_v ? a.scale[1] : a.scale[0]) + block;
+    const float old = off > 0 ? *scale : 0.f;
+    // 448 = 1.75 * 2^8: the exponent of top less 8, plus one when its significand is above 1.75
+    const int e = max(-126, int(top >> 7) - 127 - 8 + ((top & 127u) > 96u ? 1 : 0));
+    const float now = fmaxf(old, __int_as_float((e + 127) << 23));
+    const float ratio = old / now;
+    uint8_t* codes = (is_v ? a.codes[1] : a.codes[0]) + block * (int64_t(ps) * D);
+    if (off > 0 && now > old) {   // the codes before, in the new unit
+      for (int v = tid; v < off * D / 16; v += NT) {
+        uint4* p = reinterpret_cast<uint4*>(codes) + v;
+        const uint4 c = *p;
+        uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 lo = float2_of_e4m3(w[j]), hi = float2_of_e4m3(w[j] >> 16);
+          w[j] = e4m3x4(lo.x * ratio, lo.y * ratio, hi.x * ratio, hi.y * ratio);
+        }
+        *p = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    // a power of two has an exact reciprocal; a scale that a caller wrote may be another
+    const bool pow2 = (__float_as_int(now) & 0x7fffff) == 0;
+    const float inv = 1.f / now;
+    int hi8[8], lo8[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) hi8[j] = -128, lo8[j] = 127;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = tid + i * NT;
+      if (v < vecs) {
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f[2 * j] = __uint_as_float(w[j] << 16);
+          f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = pow2 ? f[j] * inv : f[j] / now;
+        const uint32_t c0 = e4m3x4(f[0], f[1], f[2], f[3]), c1 = e4m3x4(f[4], f[5], f[6], f[7]);
+        *reinterpret_cast<uint2*>(codes + s_run[v >> vshift].y * D + (v & (vd - 1)) * 8) = make_uint2(c0, c1);
+        if (bound) {
+          const uint32_t cc[4] = {c0, c0 >> 16, c1, c1 >> 16};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 q = float2_of_e4m3(cc[j]);   // NaN converts to 0
+            hi8[2 * j] = max(hi8[2 * j], __float2int_ru(q.x * 0.25f));
+            lo8[2 * j] = min(lo8[2 * j], __float2int_rd(q.x * 0.25f));
+            hi8[2 * j + 1] = max(hi8[2 * j + 1], __float2int_ru(q.y * 0.25f));
+            lo8[2 * j + 1] = min(lo8[2 * j + 1], __float2int_rd(q.y * 0.25f));
+          }
+        }
+      }
+    }
+    if (bound) {
+      if (tid < vecs) {           // NT is a multiple of vd: a thread keeps its eight channels
+        const int c = (tid & (vd - 1)) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          atomicMax(&s_hi[c + j], hi8[j]);
+          atomicMin(&s_lo[c + j], lo8[j]);
+        }
+      }
+      __syncthreads();
+      int8_t* b = a.bounds + block * (2 * D);
+      for (int c = tid; c < D; c += NT) {
+        int hi = s_hi[c], lo = s_lo[c];
+        if (off > 0) {
+          hi = max(hi, __float2int_ru(float(b[c]) * ratio));
+          lo = min(lo, __float2int_rd(float(b[D + c]) * ratio));
+        }
+        b[c] = int8_t(hi);
+        b[D + c] = int8_t(lo);
+      }
+    }
+    __syncthreads();              // every thread has read the old scale
+    if (tid == 0) *scale = now;
+  }
+}
+
+// ---- gather -----------------------------------------------------------------------------------------
+// HBM-bound: 1 byte in and 2 out per value. A CTA takes 16 rows; their pages are looked up once.
+constexpr int kGatherRows = 16;
+
+struct GatherArgs {
+  const uint8_t* codes[2];
+  const float* scale[2];
+  __nv_bfloat16* out[2];
+  const int32_t* page_table;
+  const int32_t* cu_k;
+  int64_t total_k;
+  int32_t batch, max_pages, num_pages, hkv, d, shift;
+};
+
+__global__ void __launch_bounds__(256) gather_kernel(GatherArgs a) {
+  __shared__ int s_page[kGatherRows], s_off[kGatherRows];
+  const int tid = threadIdx.x;
+  const int64_t row0 = int64_t(blockIdx.x) * kGatherRows;
+  if (tid < kGatherRows) {
+    const int64_t row = row0 + tid;
+    int pg = -2, off = 0;         // -2: no row, -1: a page outside the cache
+    if (row < a.total_k) {
+      int x = 0, y = a.batch;     // the largest b with cu[b] <= row
+      while (y - x > 1) {
+        const int m = (x + y) >> 1;
+        if (a.cu_k[m] <= row) x = m; else y = m;
+      }
+      const int64_t j = row - a.cu_k[x];
+      const int64_t pi = j >> a.shift;
+      if (j >= 0 && row < a.cu_k[x + 1] && pi < a.max_pages) {
+        pg = a.page_table[int64_t(x) * a.max_pages + pi];
+        if (unsigned(pg) >= unsigned(a.num_pages)) pg = -1;
+        off = int(j) & ((1 << a.shift) - 1);
+      }
+    }
+    s_page[tid] = pg;
+    s_off[tid] = off;
+  }
+  __syncthreads();
+  const int vd = a.d >> 4, vs = 31 - __clz(vd), cols = a.hkv * vd;
+  for (int i = tid; i < kGatherRows * cols; i += 256) {
+    const int r = i / cols, c = i - r * cols, h = c >> vs, v = c & (vd - 1);
+    const int pg = s_page[r];
+    if (pg == -2) continue;
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      uint4 w = make_uint4(0, 0, 0, 0);
+      float sc = 0.f;
+      if (pg >= 0) {
+        const int64_t block = int64_t(pg) * a.hkv + h;
+        w = __ldg(reinterpret_cast<const uint4*>(a.codes[z] + ((block << a.shift) + s_off[r]) * a.d) + v);
+        sc = __ldg(a.scale[z] + block);
+      }
+      const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+      uint32_t o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 f = float2_of_e4m3(in[j >> 1] >> (16 * (j & 1)));
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * sc, f.y * sc);
+        o[j] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      uint4* p = reinterpret_cast<uint4*>(a.out[z] + ((row0 + r) * a.hkv + h) * a.d) + 2 * v;
+      p[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      p[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  }
+}
+
+// ---- page selection -----------------------------------------------------------------------------------
+// Scores. sum_c (qi > 0 ? qi hi_c : qi lo_c) is the dot product of [max(qi, 0), min(qi, 0)] with
+// [hi, lo], so a page costs one pass over its 2 d bound bytes with 4-way int8 dot products. A quad
+// of lanes takes a page (16-byte loads, 64 contiguous bytes per quad), eight pages per warp and
+// step. HBM-bound: 2 d bytes per page and KV head.
+constexpr int kScorePages = 128;  // pages per CTA
+constexpr int kMaxGroup = 64;
+
+struct SelectArgs {
+  Batch b;
+  const __nv_bfloat16* q;
+  int64_t q_stride;
+  const int8_t* bounds;
+  const float* k_scale;
+  int32_t num_pages, hkv, group;
+  int32_t sink, recent, k;
+  float* scores;
+  int32_t* selected;
+};
+
+template <int D>
+__global__ void __launch_bounds__(128) page_score_kernel(SelectArgs a) {
+  extern __shared__ uint4 s_q[];  // [group][2 D] int8, then [group] units
+  constexpr int VEC = D / 32;     // 16-byte vectors per lane and page
+  float* s_unit = reinterpret_cast<float*>(s_q + a.group * (2 * D / 16));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tok = blockIdx.x / a.hkv, h = blockIdx.x - tok * a.hkv;
+  const int p0 = blockIdx.y * kScorePages;
+  int b, pos, len;
+  if (!a.b.token(tok, b, pos, len)) return;
+  const int n = (a.b.hi(pos, len) + (1 << a.b.page_shift) - 1) >> a.b.page_shift;
+  if (p0 >= n) return;
+
+  for (int r = warp; r < a.group; r += 4) {
+    constexpr int E = D / 32;
+    const __nv_bfloat16* q = a.q + int64_t(tok) * a.q_stride + int64_t(h * a.group + r) * D + lane * E;
+    float f[E];
+    unsigned top = 0;
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      f[j] = __bfloat162float(q[j]);
+      const unsigned m = (__float_as_uint(f[j]) >> 16) & 0x7fffu;
+      if (m < 0x7f80u) top = max(top, m);
+    }
+    top = __reduce_max_sync(~0u, top);
+    // 127 = 1.984375 * 2^6: significand 126 / 128 over 1
+    const int e = max(-126, int(top >> 7) - 127 - 6 + ((top & 127u) > 126u ? 1 : 0));
+    int8_t* dst = reinterpret_cast<int8_t*>(s_q) + r * 2 * D + lane * E;
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      // 2^-e in two factors: e = -126 has a reciprocal, e up to 121 has a normal one
+      const float y = f[j] * __int_as_float((127 - e) << 23);
+      const int qi = min(127, max(-127, __float2int_rn(y)));   // NaN converts to 0
+      dst[j] = int8_t(max(qi, 0));
+      dst[D + j] = int8_t(min(qi, 0));
+    }
+    if (lane == 0) s_unit[r] = __int_as_float((e + 127) << 23);
+  }
+  __syncthreads();
+
+  const int quad = lane >> 2, t = lane & 3;
+  const int p1 = min(n, p0 + kScorePages);
+  for (int p = p0 + warp * 8 + quad; p < p0 + kScorePages; p += 32) {
+    int pg = -1;
+    if (p < p1) pg = a.b.page_table[int64_t(b) * a.b.max_pages + p];
+    const bool in = unsigned(pg) < unsigned(a.num_pages);
+    const int64_t block = in ? int64_t(pg) * a.hkv + h : 0;
+    uint4 w[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      w[i] = in ? __ldg(reinterpret_cast<const uint4*>(a.bounds + block * (2 * D)) + 4 * i + t) : make_uint4(0, 0, 0, 0);
+    const float ks = in ? __ldg(a.k_scale + block) : 0.f;
+    float best = -INFINITY;
+    for (int r = 0; r < a.group; ++r) {
+      int dot = 0;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const uint4 c = s_q[r * (2 * D / 16) + 4 * i + t];
+        dot = __dp4a(int(w[i].x), int(c.x), dot);
+        dot = __dp4a(int(w[i].y), int(c.y), dot);
+        dot = __dp4a(int(w[i].z), int(c.z), dot);
+        dot = __dp4a(int(w[i].w), int(c.w), dot);
+      }
+      dot += __shfl_xor_sync(~0u, dot, 1);
+      dot += __shfl_xor_sync(~0u, dot, 2);
+      best = fmaxf(best, float(dot) * s_unit[r]);
+    }
+    if (t == 0 && p < p1) {
+      // finite, so that the pages that are always selected stay above it
+      const float s = fminf(fmaxf(best * (4.f * ks), -3.402823466e38f), 3.402823466e38f);
+      a.scores[(int64_t(tok) * a.hkv + h) * a.b.max_pages + p] = in ? s + 0.f : -INFINITY;
+    }
+  }
+}
+
+// The k largest of n scores with ties to the lower page: the k-th largest key by four 8-bit
+// radix passes, then the pages above it and the first of those equal to it, in ascending order.
+// One CTA per token and KV head; the scores come from L2.
+constexpr int kSelectThreads = 512;
+
+__global__ void __launch_bounds__(kSelectThreads) page_select_kernel(SelectArgs a) {
+  __shared__ int s_hist[256];
+  __shared__ int s_digit, s_above;
+  __shared__ int s_eq[kSelectThreads / 32], s_gt[kSelectThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tok = blockIdx.x / a.hkv, h = blockIdx.x - tok * a.hkv;
+  int b, pos, len;
+  if (!a.b.token(tok, b, pos, len)) return;
+  const int n = (a.b.hi(pos, len) + (1 << a.b.page_shift) - 1) >> a.b.page_shift;
+  const float* scores = a.scores + (int64_t(tok) * a.hkv + h) * a.b.max_pages;
+  int32_t* out = a.selected + (int64_t(tok) * a.hkv + h) * a.k;
+  for (int i = tid; i < a.k; i += kSelectThreads)
+    if (i >= n) out[i] = -1;
+  if (n <= a.k) {
+    for (int i = tid; i < n; i += kSelectThreads) out[i] = i;
+    return;
+  }
+  auto key = [&](int p) -> uint32_t {
+    if (p < a.sink || p >= n - a.recent) return 0xffffffffu;
+    const uint32_t u = __float_as_uint(scores[p]);
+    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+  };
+  uint32_t prefix = 0, fixed = 0;
+  int rem = a.k;                  // how many of the keys that match the prefix are taken
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    if (tid < 256) s_hist[tid] = 0;
+    __syncthreads();
+    for (int p = tid; p < n; p += kSelectThreads) {
+      const uint32_t u = key(p);
+      if ((u & fixed) == prefix) atomicAdd(&s_hist[(u >> shift) & 255u], 1);
+    }
+    __syncthreads();
+    if (warp == 0) {              // lane l holds bins 255 - 8 l down to 248 - 8 l
+      int c[8], sum = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum += c[j] = s_hist[255 - 8 * lane - j];
+      int inc = sum;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(~0u, inc, o);
+        if (lane >= o) inc += x;
+      }
+      int above = inc - sum;
+      if (above < rem && inc >= rem) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (above < rem && above + c[j] >= rem) s_digit = 255 - 8 * lane - j, s_above = above;
+          above += c[j];
+        }
+      }
+    }
+    __syncthreads();
+    prefix |= uint32_t(s_digit) << shift;
+    fixed |= 255u << shift;
+    rem -= s_above;
+  }
+  int eq0 = 0, gt0 = 0;           // counts before this round's pages
+  for (int base = 0; base < n; base += kSelectThreads) {
+    const int p = base + tid;
+    const uint32_t u = p < n ? key(p) : 0u;
+    const bool gt = p < n && u > prefix, eq = p < n && u == prefix;
+    const unsigned mg = __ballot_sync(~0u, gt), me = __ballot_sync(~0u, eq);
+    if (lane == 0) s_gt[warp] = __popc(mg), s_eq[warp] = __popc(me);
+    __syncthreads();
+    int g = gt0, e = eq0;
+    for (int w = 0; w < kSelectThreads / 32; ++w) {
+      if (w < warp) g += s_gt[w], e += s_eq[w];
+      gt0 += s_gt[w];
+      eq0 += s_eq[w];
+    }
+    const unsigned below = (1u << lane) - 1u;
+    g += __popc(mg & below);
+    e += __popc(me & below);
+    if (gt || (eq && e < rem)) out[g + min(e, rem)] = p;
+    __syncthreads();
+  }
+}
+
+}  // namespace
+}  // namespace kv8
+
+using namespace kv8;
+
+extern "C" {
+
+attn_status_t attn_page_tables(const attn_page_tables_t* t, attn_stream_t stream) {
+  if (!t) return ATTN_ERR_INVALID_ARG;
+  const int shift = shift_of(t->page_size);
+  if (shift < 0 || t->batch > 16384) return ATTN_ERR_UNSUPPORTED;
+  if (t->batch < 0 || t->max_pages_per_seq < 1 || t->num_pages < 1 || t->max_tokens < 0) return ATTN_ERR_INVALID_ARG;
+  if (int64_t(t->batch) * t->max_pages_per_seq >= (int64_t(1) << 31) ||
+      int64_t(t->num_pages) * t->page_size >= (int64_t(1) << 31))
+    return ATTN_ERR_INVALID_ARG;
+  if (!t->free_pages || !t->free_state || !t->next_state || !t->cu_seqlens_q) return ATTN_ERR_INVALID_ARG;
+  if (t->batch && (!t->page_table || !t->old_lens || !t->new_lens || !t->kv_lens)) return ATTN_ERR_INVALID_ARG;
+  if (t->max_tokens && !t->slots) return ATTN_ERR_INVALID_ARG;
+  // every array of its own, but that old_lens and new_lens (only read) may be one
+  const struct { const void* p; int64_t n; } all[] = {
+      {t->old_lens, t->batch}, {t->new_lens, t->batch}, {t->free_state, 4}, {t->next_state, 4}, {t->kv_lens, t->batch},
+      {t->cu_seqlens_q, int64_t(t->batch) + 1}, {t->slots, t->max_tokens}, {t->positions, t->max_tokens},
+      {t->free_pages, t->num_pages}, {t->page_table, int64_t(t->batch) * t->max_pages_per_seq}};
+  for (int i = 0; i < 10; ++i) {
+    if (misaligned(all[i].p, 4)) return ATTN_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (!(i == 1 && j == 0) && overlap(all[i].p, 4 * all[i].n, all[j].p, 4 * all[j].n)) return ATTN_ERR_INVALID_ARG;
+  }
+  const int work = std::max(t->batch + 1, t->max_tokens);
+  const int threads = work <= 256 ? 256 : 1024;
+  const int grid = std::min(148, (work + threads - 1) / threads);
+  const size_t smem = size_t(3) * (t->batch + 1) * sizeof(int);
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  page_tables_kernel<<<grid, threads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(*t, shift);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+attn_status_t attn_kv8_append(const attn_kv8_cache_t* c, const void* k_new, int64_t k_stride, const void* v_new,
+                              int64_t v_stride, const int32_t* slots, int32_t num_tokens, attn_stream_t stream) {
+  const attn_status_t st = check_cache(c);
+  if (st != ATTN_OK) return st;
+  if (num_tokens < 0) return ATTN_ERR_INVALID_ARG;
+  if (num_tokens == 0) return ATTN_OK;
+  const int64_t row = int64_t(c->hkv) * c->head_dim;
+  if (!k_new || !v_new || !slots || misaligned(k_new, 16) || misaligned(v_new, 16) || misaligned(slots, 4))
+    return ATTN_ERR_INVALID_ARG;
+  if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8) return ATTN_ERR_INVALID_ARG;
+  AppendArgs a{};
+  a.x[0] = static_cast<const __nv_bfloat16*>(k_new);
+  a.x[1] = static_cast<const __nv_bfloat16*>(v_new);
+  a.stride[0] = k_stride;
+  a.stride[1] = v_stride;
+  a.codes[0] = static_cast<uint8_t*>(c->k);
+  a.codes[1] = static_cast<uint8_t*>(c->v);
+  a.scale[0] = c->k_scale;
+  a.scale[1] = c->v_scale;
+  a.bounds = c->k_bounds;
+  a.slots = slots;
+  a.tokens = num_tokens;
+  a.hkv = c->hkv;
+  a.d = c->head_dim;
+  a.shift = shift_of(c->page_size);
+  a.num_slots = c->num_pages * c->page_size;
+  // tokens per CTA: enough that the grid is about one wave of 148 x 16 CTAs, at most a page
+  int span = 1;
+  while (span < c->page_size && int64_t(num_tokens) * c->hkv * 2 >= int64_t(2 * span) * 148 * 16) span *= 2;
+  a.span = span;
+  const dim3 grid((num_tokens + span - 1) / span, c->hkv, 2);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int vecs = c->page_size * c->head_dim / 8;   // 16-byte vectors of a full page
+  switch (vecs) {
+    case 128: append_kernel<128, 1><<<grid, 128, 0, s>>>(a); break;
+    case 256: append_kernel<128, 2><<<grid, 128, 0, s>>>(a); break;
+    case 512: append_kernel<128, 4><<<grid, 128, 0, s>>>(a); break;
+    case 1024: append_kernel<128, 8><<<grid, 128, 0, s>>>(a); break;
+    case 2048: append_kernel<256, 8><<<grid, 256, 0, s>>>(a); break;
+    default: append_kernel<256, 16><<<grid, 256, 0, s>>>(a); break;
+  }
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+attn_status_t attn_kv8_gather(const attn_kv8_cache_t* c, const int32_t* page_table, int32_t max_pages_per_seq,
+                              const int32_t* cu_seqlens_k, int32_t batch, int64_t total_k, void* k_out, void* v_out,
+                              attn_stream_t stream) {
+  const attn_status_t st = check_cache(c);
+  if (st != ATTN_OK) return st;
+  if (batch < 0 || total_k < 0 || max_pages_per_seq < 1) return ATTN_ERR_INVALID_ARG;
+  if (batch == 0 || total_k == 0) return ATTN_OK;
+  if (!page_table || !cu_seqlens_k || !k_out || !v_out || total_k >= (int64_t(1) << 31)) return ATTN_ERR_INVALID_ARG;
+  if (misaligned(k_out, 16) || misaligned(v_out, 16) || misaligned(page_table, 4) || misaligned(cu_seqlens_k, 4))
+    return ATTN_ERR_INVALID_ARG;
+  GatherArgs a{};
+  a.codes[0] = static_cast<const uint8_t*>(c->k);
+  a.codes[1] = static_cast<const uint8_t*>(c->v);
+  a.scale[0] = c->k_scale;
+  a.scale[1] = c->v_scale;
+  a.out[0] = static_cast<__nv_bfloat16*>(k_out);
+  a.out[1] = static_cast<__nv_bfloat16*>(v_out);
+  a.page_table = page_table;
+  a.cu_k = cu_seqlens_k;
+  a.total_k = total_k;
+  a.batch = batch;
+  a.max_pages = max_pages_per_seq;
+  a.num_pages = c->num_pages;
+  a.hkv = c->hkv;
+  a.d = c->head_dim;
+  a.shift = shift_of(c->page_size);
+  const unsigned grid = unsigned((total_k + kGatherRows - 1) / kGatherRows);
+  gather_kernel<<<grid, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+attn_status_t attn_kv8_select(const attn_kv8_plan_t* p, const attn_kv8_cache_t* c, const attn_kv8_batch_t* b,
+                              int32_t sink, int32_t recent, float* scores, int32_t* selected, int32_t n_selected,
+                              attn_stream_t stream) {
+  const attn_status_t st = check_batch(p, c, b);
+  if (st != ATTN_OK) return st;
+  if (p->mask == ATTN_MASK_SLIDING_WINDOW || p->hq / p->hkv > kMaxGroup) return ATTN_ERR_UNSUPPORTED;
+  if (sink < 0 || recent < 1 || int64_t(sink) + recent > n_selected) return ATTN_ERR_INVALID_ARG;
+  if (b->total_q == 0 || b->batch == 0) return ATTN_OK;
+  if (!c->k_bounds || !scores || !selected || misaligned(scores, 4) || misaligned(selected, 4)) return ATTN_ERR_INVALID_ARG;
+  const int64_t rows = int64_t(b->total_q) * p->hkv;
+  const int64_t chunks = (int64_t(b->max_pages_per_seq) + kScorePages - 1) / kScorePages;
+  if (rows >= (int64_t(1) << 31) || chunks > 65535) return ATTN_ERR_INVALID_ARG;
+  SelectArgs a{};
+  a.b = batch_of(p, b);
+  a.q = static_cast<const __nv_bfloat16*>(b->q);
+  a.q_stride = b->q_stride;
+  a.bounds = c->k_bounds;
+  a.k_scale = c->k_scale;
+  a.num_pages = c->num_pages;
+  a.hkv = p->hkv;
+  a.group = p->hq / p->hkv;
+  a.sink = sink;
+  a.recent = recent;
+  a.k = n_selected;
+  a.scores = scores;
+  a.selected = selected;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const dim3 grid{unsigned(rows), unsigned(chunks)};
+  const size_t smem = size_t(a.group) * (2 * p->d + 4);
+  if (p->d == 64) page_score_kernel<64><<<grid, 128, smem, s>>>(a);
+  else if (p->d == 128) page_score_kernel<128><<<grid, 128, smem, s>>>(a);
+  else page_score_kernel<256><<<grid, 128, smem, s>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  page_select_kernel<<<unsigned(rows), kSelectThreads, 0, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // extern "C"

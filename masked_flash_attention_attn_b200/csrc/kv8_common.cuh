@@ -1,0 +1,143 @@
+// Shared by the kernels of the 8-bit paged K/V cache (attn_kv8.cu, attn_kv8_fwd.cu): the
+// query batch as the kernels see it, e4m3 conversions, and host-side argument checks.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "attn_kv8.h"
+
+struct attn_kv8_plan {
+  int32_t hq = 0, hkv = 0, d = 0, page_size = 0, page_shift = 0;
+  float scale = 0.f;
+  int32_t mask = 0, window = 0;
+  int32_t ng = 1;                 // row tile of the attention kernel: 8 ng rows
+  int32_t grid = 0;               // persistent CTAs
+  int32_t device = 0;
+  void* ws = nullptr;             // partial results and counters
+  float* part_o = nullptr;        // [2 grid][8 ng][d]
+  float* part_ml = nullptr;       // [2 grid][8 ng][2]
+  uint32_t* counters = nullptr;   // [grid], zero between launches
+};
+
+namespace kv8 {
+
+// The query tokens of a call and how they see the keys.
+struct Batch {
+  const int32_t* page_table;
+  const int32_t* kv_lens;
+  const int32_t* cu_q;            // null: one token per request
+  int32_t batch, total_q, max_pages, page_shift;
+  int32_t mask, window;
+  __device__ __forceinline__ int len(int b) const {
+    const long long cap = (long long)max_pages << page_shift;
+    const int l = kv_lens[b];
+    return l < 0 ? 0 : (l > cap ? int(cap) : l);
+  }
+  __device__ __forceinline__ int cu(int b) const {
+    const int c = cu_q[b];
+    return c < 0 ? 0 : (c > total_q ? total_q : c);
+  }
+  // keys [lo, hi) that the token at position pos of a request of `n` tokens sees
+  __device__ __forceinline__ int hi(int pos, int n) const {
+    if (mask == ATTN_MASK_FULL) return n;
+    return pos < 0 ? 0 : (pos + 1 < n ? pos + 1 : n);
+  }
+  __device__ __forceinline__ int lo(int pos) const {
+    return mask == ATTN_MASK_SLIDING_WINDOW && pos >= window ? pos - window + 1 : 0;
+  }
+  // request of token t: true and its position and length, or false behind the last request
+  __device__ __forceinline__ bool token(int t, int& b, int& pos, int& n) const {
+    int i = 0, nq = 1;
+    if (cu_q == nullptr) {
+      b = t;
+    } else {
+      int x = 0, y = batch;       // the largest b with cu[b] <= t
+      while (y - x > 1) {
+        const int m = (x + y) >> 1;
+        if (cu(m) <= t) x = m; else y = m;
+      }
+      b = x;
+      i = t - cu(b);
+      nq = cu(b + 1) - cu(b);
+      if (i < 0 || i >= nq) return false;
+    }
+    n = len(b);
+    pos = n - nq + i;
+    return true;
+  }
+};
+
+// two e4m3 codes (low byte first) -> two halves; exact
+__device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(uint16_t(two)));
+  return r;
+}
+
+__device__ __forceinline__ float2 float2_of_e4m3(uint32_t two) {
+  const uint32_t h = half2_of_e4m3(two);
+  float2 f;
+  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(f.x), "=f"(f.y) : "r"(h));
+  return f;
+}
+
+// Four fp32 -> four e4m3, `a` in the lowest byte: round to nearest even, saturating at +-448,
+// NaN kept.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return uint32_t(lo) | (uint32_t(hi) << 16);
+}
+
+// ---- host checks ------------------------------------------------------------------------------
+inline bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+inline bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
+  return x && y && na > 0 && nb > 0 && x < y + nb && y < x + na;
+}
+inline int shift_of(int32_t page_size) {
+  return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : page_size == 128 ? 7 : -1;
+}
+
+inline attn_status_t check_cache(const attn_kv8_cache_t* c) {
+  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale) return ATTN_ERR_INVALID_ARG;
+  if (shift_of(c->page_size) < 0) return ATTN_ERR_UNSUPPORTED;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return ATTN_ERR_UNSUPPORTED;
+  if (c->num_pages < 1 || c->hkv < 1 || c->hkv > 65535) return ATTN_ERR_INVALID_ARG;
+  if (int64_t(c->num_pages) * c->page_size >= (int64_t(1) << 31)) return ATTN_ERR_INVALID_ARG;
+  if (misaligned(c->k, 16) || misaligned(c->v, 16) || misaligned(c->k_scale, 4) || misaligned(c->v_scale, 4) ||
+      misaligned(c->k_bounds, 16))
+    return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+inline attn_status_t check_batch(const attn_kv8_plan_t* p, const attn_kv8_cache_t* c, const attn_kv8_batch_t* b) {
+  if (!p || !b) return ATTN_ERR_INVALID_ARG;
+  const attn_status_t st = check_cache(c);
+  if (st != ATTN_OK) return st;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (dev != p->device) return ATTN_ERR_INVALID_ARG;
+  if (c->hkv != p->hkv || c->head_dim != p->d || c->page_size != p->page_size) return ATTN_ERR_INVALID_ARG;
+  if (b->batch < 0 || b->total_q < 0 || b->max_pages_per_seq < 1) return ATTN_ERR_INVALID_ARG;
+  if (int64_t(b->total_q) * p->hq >= (int64_t(1) << 31)) return ATTN_ERR_INVALID_ARG;
+  if (int64_t(b->max_pages_per_seq) * p->page_size >= (int64_t(1) << 31)) return ATTN_ERR_INVALID_ARG;
+  if (!b->cu_seqlens_q && b->total_q != b->batch) return ATTN_ERR_INVALID_ARG;
+  if (b->total_q == 0 || b->batch == 0) return ATTN_OK;
+  if (!b->q || !b->page_table || !b->kv_lens) return ATTN_ERR_INVALID_ARG;
+  if (b->q_stride < int64_t(p->hq) * p->d || b->q_stride % 8) return ATTN_ERR_INVALID_ARG;
+  if (misaligned(b->q, 16) || misaligned(b->cu_seqlens_q, 4) || misaligned(b->page_table, 4) || misaligned(b->kv_lens, 4))
+    return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+inline Batch batch_of(const attn_kv8_plan_t* p, const attn_kv8_batch_t* b) {
+  return Batch{b->page_table, b->kv_lens, b->cu_seqlens_q, b->batch, b->total_q, b->max_pages_per_seq, p->page_shift,
+               p->mask, p->window};
+}
+
+}  // namespace kv8
