@@ -36,11 +36,14 @@ extern "C" {
 
 /* The cache. All pointers are DEVICE pointers, 16-byte aligned (k_scale, v_scale: 4-byte).
  * The block of one page and head is contiguous, so it is read in whole lines whatever hkv is.
- * The value of a code is code * scale, code one of the e4m3 values (no infinities, max 448). */
+ * The value of a code is code * scale, code one of the finite e4m3 values (max 448). A NaN is kept
+ * in the scale: a page and head whose scale is NaN read as NaN. The codes 0x7F and 0xFF are
+ * never written by attn_kv8_append(); what a call makes of one in a token's place is undefined,
+ * bytes in places that no token holds are never used. */
 typedef struct {
   void* k;              /* e4m3 [num_pages][hkv][page_size][head_dim] */
   void* v;              /* the same */
-  float* k_scale;       /* fp32 [num_pages][hkv], >= 0 */
+  float* k_scale;       /* fp32 [num_pages][hkv], >= 0 or NaN */
   float* v_scale;       /* the same */
   int8_t* k_bounds;     /* int8 [num_pages][hkv][2][head_dim]: per channel the largest (row 0) and the
                            smallest (row 1) K code of the page in steps of 4 codes, rounded
@@ -99,9 +102,11 @@ attn_status_t attn_page_tables(const attn_page_tables_t* tables, attn_stream_t s
  * Per page and head, with amax the largest finite |x| of its new tokens:
  *     scale = max(scale before, 2^e), e >= -126 the least with amax <= 448 * 2^e,
  * (a page whose place 0 is among the tokens is new: its scale before counts as 0);
- *     code = x / scale rounded to nearest even, infinities to +-448, NaN kept,
+ *     code = x / scale rounded to nearest even, infinities to +-448,
  * and if the scale grew, the codes before become code * before / scale, rounded likewise
  * (exact for powers of two, but for subnormal codes). k_bounds is kept up in the same way.
+ * A NaN among the new values makes the scale NaN until place 0 of the page is written again;
+ * other pages, heads and (K or V) are not touched by it.
  * Errors: INVALID_ARG, UNSUPPORTED (page_size, head_dim), CUDA. */
 attn_status_t attn_kv8_append(const attn_kv8_cache_t* cache, const void* k_new, int64_t k_stride, const void* v_new,
                               int64_t v_stride, const int32_t* slots, int32_t num_tokens, attn_stream_t stream);
@@ -171,7 +176,7 @@ attn_status_t attn_kv8_fwd(const attn_kv8_plan_t* plan, const attn_kv8_cache_t* 
  * rounded to nearest even (infinities +-127, NaN 0), over the query heads a of h,
  *     score = 4 * k_scale * max_a 2^e sum_c (qi[c] > 0 ? qi[c] * bounds[0][c] : qi[c] * bounds[1][c]),
  * exact integers below 2^24, so equal inputs select equal pages; ties go to the lower
- * page. scores (fp32 [total_q][hkv][max_pages_per_seq]) receives the scores of the pages a token
+ * page, and a page whose scale is NaN has the largest finite score. scores (fp32 [total_q][hkv][max_pages_per_seq]) receives the scores of the pages a token
  * sees; its other entries are left as they were. The plan's mask must be CAUSAL (or FULL: each
  * token then sees all kv_len tokens). 0 <= sink, 1 <= recent, sink + recent <= n_selected.
  * Errors: INVALID_ARG, UNSUPPORTED (SLIDING_WINDOW plan), CUDA. */

@@ -165,11 +165,21 @@ def _ptr(a) -> Optional[int]:
     return a.data_ptr()
 
 
+_raw_stream = None
+
+
 def _stream(stream) -> Optional[int]:
-    if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
-    return getattr(stream, "cuda_stream", stream)
+    if stream is not None:
+        return getattr(stream, "cuda_stream", stream)
+    global _raw_stream
+    import torch
+    if _raw_stream is None:
+        if not torch.cuda.is_available():
+            return None
+        # the raw handle of a device's current stream; building a torch Stream object for it takes ~3 us
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _raw_stream(torch.cuda.current_device())
 
 
 class _Marshal:

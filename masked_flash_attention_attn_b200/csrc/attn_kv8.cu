@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(NT) append_kernel(AppendArgs a) {
 
     uint4 x[NV];
     unsigned top = 0;             // the largest finite |x|, as bf16 bits
+    bool nan = false;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = tid + i * NT;
@@ -248,11 +249,12 @@ __global__ void __launch_bounds__(NT) append_kernel(AppendArgs a) {
         const unsigned lo = w[j] & 0x7fffu, hi = (w[j] >> 16) & 0x7fffu;
         if (lo < 0x7f80u) top = max(top, lo);
         if (hi < 0x7f80u) top = max(top, hi);
+        nan |= lo > 0x7f80u || hi > 0x7f80u;
       }
     }
     top = __reduce_max_sync(~0u, top);
     if ((tid & 31) == 0) s_max[tid >> 5] = top;
-    __syncthreads();
+    nan = __syncthreads_or(nan);
 #pragma unroll
     for (int i = 0; i < NT / 32; ++i) top = max(top, s_max[i]);
 
@@ -261,10 +263,11 @@ __global__ void __launch_bounds__(NT) append_kernel(AppendArgs a) {
     const float old = off > 0 ? *scale : 0.f;
     // 448 = 1.75 * 2^8: the exponent of top less 8, plus one when its significand is above 1.75
     const int e = max(-126, int(top >> 7) - 127 - 8 + ((top & 127u) > 96u ? 1 : 0));
-    const float now = fmaxf(old, __int_as_float((e + 127) << 23));
-    const float ratio = old / now;
+    nan |= old != old;            // a NaN stays with its page until place 0 is written again
+    const float unit = __int_as_float((e + 127) << 23), now = nan ? unit : fmaxf(old, unit);
+    const float ratio = nan ? 1.f : old / now;
     uint8_t* codes = (is_v ? a.codes[1] : a.codes[0]) + block * (int64_t(ps) * D);
-    if (off > 0 && now > old) {   // the codes before, in the new unit
+    if (off > 0 && ratio < 1.f) { // the codes before, in the new unit
       for (int v = tid; v < off * D / 16; v += NT) {
         uint4* p = reinterpret_cast<uint4*>(codes) + v;
         const uint4 c = *p;
@@ -295,14 +298,14 @@ __global__ void __launch_bounds__(NT) append_kernel(AppendArgs a) {
           f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = pow2 ? f[j] * inv : f[j] / now;
+        for (int j = 0; j < 8; ++j) f[j] = f[j] != f[j] ? 0.f : pow2 ? f[j] * inv : f[j] / now;
         const uint32_t c0 = e4m3x4(f[0], f[1], f[2], f[3]), c1 = e4m3x4(f[4], f[5], f[6], f[7]);
         *reinterpret_cast<uint2*>(codes + s_run[v >> vshift].y * D + (v & (vd - 1)) * 8) = make_uint2(c0, c1);
         if (bound) {
           const uint32_t cc[4] = {c0, c0 >> 16, c1, c1 >> 16};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 q = float2_of_e4m3(cc[j]);   // NaN converts to 0
+            const float2 q = float2_of_e4m3(cc[j]);
             hi8[2 * j] = max(hi8[2 * j], __float2int_ru(q.x * 0.25f));
             lo8[2 * j] = min(lo8[2 * j], __float2int_rd(q.x * 0.25f));
             hi8[2 * j + 1] = max(hi8[2 * j + 1], __float2int_ru(q.y * 0.25f));
@@ -333,7 +336,7 @@ __global__ void __launch_bounds__(NT) append_kernel(AppendArgs a) {
       }
     }
     __syncthreads();              // every thread has read the old scale
-    if (tid == 0) *scale = now;
+    if (tid == 0) *scale = nan ? __int_as_float(0x7fffffff) : now;
   }
 }
 
@@ -493,8 +496,10 @@ __global__ void __launch_bounds__(128) page_score_kernel(SelectArgs a) {
       best = fmaxf(best, float(dot) * s_unit[r]);
     }
     if (t == 0 && p < p1) {
-      // finite, so that the pages that are always selected stay above it
-      const float s = fminf(fmaxf(best * (4.f * ks), -3.402823466e38f), 3.402823466e38f);
+      // finite, so that the pages that are always selected stay above it; a page that holds a NaN
+      // comes first of the others, so that the NaN shows
+      float s = best * (4.f * ks);
+      s = s != s ? 3.402823466e38f : fminf(fmaxf(s, -3.402823466e38f), 3.402823466e38f);
       a.scores[(int64_t(tok) * a.hkv + h) * a.b.max_pages + p] = in ? s + 0.f : -INFINITY;
     }
   }

@@ -10,15 +10,21 @@
 // decode step fill a tile (as the 128-row side of a tcgen05 MMA they would use 6 % of it).
 //
 // What bounds it: HBM. 2 d bytes per key and KV head are read once; at the measured copy rate
-// an SM receives ~23 bytes per clock, against ~1 instruction slot per 2 bytes here.
+// an SM receives ~23 bytes per clock. The conversion comes next: cvt.f16x2.e4m3x2 measured ~4 clocks
+// of the SM per warp instruction (profiled: the XU pipe 73 % busy at 3.1 TB/s, nothing else above
+// 27 %), which alone caps the stream at 16 bytes per clock. So K and half of V are converted by
+// shifts and logic: the code's sign, exponent and mantissa moved into an fp16 give code / 256,
+// exactly (subnormals too), and the factor goes into the scales.
 //
-// Layout. A step is 16 keys (a page holds a whole number of them). The 16 bytes that a lane
-// loads are the ones its MMA fragments need, because the order of channels in the dot product
-// and of output channels over the tile rows is free: K: lane (g, t) takes bytes 64 i + 16 t of
-// keys g and g + 8; V: bytes [d/8 g, d/8 (g+1)) of keys 2t, 2t+1, 2t+8, 2t+9. So every lane copies
-// its own bytes into its own slots of a ring in shared memory (cp.async) and reads them back: no
-// barrier, no bank conflict, no swizzle, and the loads of several steps in flight without
-// registers. P passes from the accumulator layout of S^T to the operand layout of P^T by movmatrix.
+// Layout. A step is 16 keys (a page holds a whole number of them): 16 d contiguous bytes of K and
+// of V. A warp copies them by cp.async, 512 contiguous bytes per instruction, into its own ring
+// of stages (no barrier but __syncwarp). Copying straight into fragment order instead (each
+// lane the bytes it needs, 64-byte pieces) measured 5.0 TB/s against 6.8 TB/s for this order. The
+// order of channels in the dot product and of output channels over the tile rows is free, so
+// every read is of 16 bytes that are one lane's fragments: K: lane (g, t) bytes 64 i + 16 t of keys g
+// and g + 8; V: bytes 16 g (+ 128) of keys 2t, 2t+1, 2t+8, 2t+9. 16-byte chunks of a row are swizzled
+// so that both reads are free of bank conflicts. P passes from the accumulator layout of S^T to
+// the operand layout of P^T by movmatrix.
 //
 // Work. The steps of all (request, KV head, row tile) items form one line, cut into equal
 // parts for the persistent CTAs (each scans the lengths itself); within a CTA the warps take
@@ -77,19 +83,20 @@ struct Cfg {
   static constexpr int QPITCH = D + 8;                 // halves; the pad spreads rows over banks
   static constexpr int OFF_Q = RING > MERGE ? RING : MERGE;
   static constexpr int OFF_META = OFF_Q + ROWS * QPITCH * 2;
-  static constexpr int OFF_ML = OFF_META + kWarps * 64 * 16;
+  static constexpr int OFF_SCALE = OFF_META + kWarps * 64 * 8;    // [warp][stage] k_scale, v_scale
+  static constexpr int OFF_ML = OFF_SCALE + kWarps * STAGES * 8;
   static constexpr int OFF_ROW = OFF_ML + kWarps * ROWS * 8;      // [ROWS] factor, hi, lo, out row
   static constexpr int SMEM = OFF_ROW + ROWS * 16;
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return uint32_t(__cvta_generic_to_shared(p)); }
 
-// `bytes` of the source are read, the rest of the 16 (or 8) are zeros
+// `bytes` of the source are read, the rest of the 16 (or 4) are zeros
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void cp8(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -128,6 +135,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// The codes in the odd / even bytes of w as two halves (lower byte first) of code / 256: the
+// sign stays on top, exponent and mantissa move down by one bit (fp16 has a fifth exponent bit).
+__device__ __forceinline__ uint32_t half2_of_odd(uint32_t w) { return (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u); }
+__device__ __forceinline__ uint32_t half2_of_even(uint32_t w) { return ((w << 8) & 0x80008000u) | ((w << 7) & 0x3f803f80u); }
 
 // A unit of the work line: a request, or with selected pages a query token.
 struct Unit {
@@ -193,10 +205,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
   }
-  const long long G = min((long long)gridDim.x, total);
-  if (blockIdx.x >= G) return;
-  auto start_of = [&](long long c) { return total * c / G; };
-  auto cta_of = [&](long long x) { return ((x + 1) * G - 1) / total; };   // the CTA whose part holds x
+  const int G = int(min((long long)gridDim.x, total));
+  if (int(blockIdx.x) >= G) return;
+  // the first `more` CTAs take part + 1 chunks, the others part
+  auto divide = [](long long x, long long y) { return (x | y) >> 31 ? x / y : (long long)(unsigned(x) / unsigned(y)); };
+  const long long part = divide(total, G);
+  const int more = int(total - part * G);
+  auto start_of = [&](int c) { return c * part + min(c, more); };
+  auto cta_of = [&](long long x) {                // the CTA whose part holds x
+    const long long wide = more * (part + 1);
+    return int(x < wide ? divide(x, part + 1) : more + divide(x - wide, part));
+  };
   const long long line0 = start_of(blockIdx.x), line1 = start_of(blockIdx.x + 1);
   long long first = before + inc - mine;          // the line where this thread's units begin
   if (first <= line0 && line0 < first + mine) {
@@ -215,12 +234,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
   long long off = s_found;                        // chunk offset inside the unit
 
   __half* s_q = reinterpret_cast<__half*>(smem + C::OFF_Q);
-  int4* s_meta = reinterpret_cast<int4*>(smem + C::OFF_META) + warp * 64;
+  int2* s_meta = reinterpret_cast<int2*>(smem + C::OFF_META) + warp * 64;
+  const float2* s_scale = reinterpret_cast<const float2*>(smem + C::OFF_SCALE) + warp * S;
+  const uint32_t scale_addr = base + C::OFF_SCALE + warp * (S * 8) + (lane & 1) * 4;
   float2* s_ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
   int4* s_row = reinterpret_cast<int4*>(smem + C::OFF_ROW);
   float* s_o = reinterpret_cast<float*>(smem);
-  const uint32_t ring = base + warp * (S * C::STAGE_BYTES) + lane * 16;
-  const uint32_t ring_v8 = base + warp * (S * C::STAGE_BYTES) + lane * 8;   // D == 64: 8-byte V slots
+  // Chunk c (16 bytes) of a stage's row r lies at chunk c ^ s(r), s(r) = (((r >> 1) & 3) ^ ((r & 1) << 1)) << 1
+  // (rows of 64 bytes: c ^ ((r >> 1) & 3)): of the eight lanes of one shared-memory phase, the K reads
+  // have two neighbouring rows and four neighbouring chunks, the V reads four rows two apart and two
+  // neighbouring chunks; both hit all eight chunks of a 128-byte line (64-byte rows: V two ways).
+  const uint32_t ring = base + warp * (S * C::STAGE_BYTES);
+  const int wr = lane / (D / 16), wc = lane % (D / 16);   // copies: row (of 512 bytes) and chunk of the lane
+  const uint32_t copy_to = ring + wr * D + ((D == 64 ? wc ^ ((wr >> 1) & 3) : wc ^ ((((wr >> 1) & 3) ^ ((wr & 1) << 1)) << 1)) << 4);
+  const uint32_t k_at = ring + g * D + ((D == 64 ? t ^ ((g >> 1) & 3) : t ^ ((((g >> 1) & 3) ^ ((g & 1) << 1)) << 1)) << 4);
+  const uint32_t v_at = ring + 16 * D + 2 * t * D + (D == 64 ? (((g >> 1) ^ t) << 4) + (g & 1) * 8 : (g ^ (t << 1)) << 4);
 
   for (long long line = line0; line < line1;) {
     const Unit x = unit_of<ROWS>(a, unit);
@@ -234,6 +262,64 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
     const int c1 = int(min((long long)x.chunks, c0 + (line1 - line)));
     const int h = item / x.tiles, tile = item - h * x.tiles;
     const int rows = int(min((long long)ROWS, (long long)x.nq * a.group - (long long)tile * ROWS));
+
+    // ---- the warp's steps: the i-th is step (c0 + i) kWarps + warp of the unit ----
+    const int i0 = int(int64_t(tile) * ROWS / a.group), i1 = int((int64_t(tile) * ROWS + rows - 1) / a.group);
+    const int hi_all = a.b.hi(x.pos0 + i0, x.len), hi_any = a.b.hi(x.pos0 + i1, x.len);
+    const int lo_any = a.b.lo(x.pos0 + i0), lo_all = a.b.lo(x.pos0 + i1);
+    const int count = c1 - c0;
+    // first key (-1: skip the step) and page (-1: outside the cache, zeros) of the 32 steps from i on
+    auto load_meta = [&](int i) {
+      const int st = (c0 + i + lane) * kWarps + warp;
+      int key = -1, pg = -1;
+      if (i + lane < count && st < x.steps) {
+        int page, inner;
+        if (a.selected) {
+          const int j = st >> (a.b.page_shift - 4);
+          page = __ldg(a.selected + (int64_t(x.tok0) * a.hkv + h) * a.n_selected + j);
+          inner = (st << 4) & (ps - 1);
+        } else {
+          const int kk = x.key0 + st * kStep;
+          page = kk >> a.b.page_shift;
+          inner = kk & (ps - 1);
+        }
+        if (unsigned(page) < unsigned(a.b.max_pages)) {
+          key = (page << a.b.page_shift) + inner;
+          if (key >= hi_any || key + kStep <= lo_any) {
+            key = -1;
+          } else {
+            pg = __ldg(a.b.page_table + int64_t(x.b) * a.b.max_pages + page);
+            if (unsigned(pg) >= unsigned(a.num_pages)) pg = -1;
+          }
+        }
+      }
+      s_meta[(i + lane) & 63] = make_int2(key, pg);
+      __syncwarp();
+    };
+    auto issue = [&](int i) {
+      if (i < count) {
+        if ((i & 31) == 0) load_meta(i);
+        const int2 m = s_meta[i & 63];
+        if (m.x >= 0) {
+          const int bytes = m.y >= 0 ? 16 : 0;
+          const int64_t block = int64_t(max(m.y, 0)) * a.hkv + h;
+          const int64_t o = (block << a.b.page_shift) + (m.x & (ps - 1));
+          const uint8_t* kp = a.k + o * D + lane * 16;
+          const uint8_t* vp = a.v + o * D + lane * 16;
+          const uint32_t st = uint32_t(i % S) * C::STAGE_BYTES;
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) {      // s() of the rows that the j-th 512 bytes hold
+            const uint32_t flip = D == 128 ? (j & 1) * 64 : D == 256 ? (j & 3) * 32 : 0;
+            cp16((copy_to ^ flip) + st + j * 512, kp + j * 512, bytes);
+            cp16((copy_to ^ flip) + st + 16 * D + j * 512, vp + j * 512, bytes);
+          }
+          if (lane < 2) cp4(scale_addr + uint32_t(i % S) * 8, (lane ? a.v_scale : a.k_scale) + block, bytes >> 2);
+        }
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) issue(i);
 
     // ---- rows of the tile: query in fp16, score factor, visible keys ----
     for (int r = warp; r < ROWS; r += kWarps) {
@@ -265,17 +351,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
       const int e = top >= 0x7f80u ? 0 : min(100, 14 - (int(top >> 7) - 127));
       const float f2 = __int_as_float((127 + e) << 23);
       __half* dst = s_q + r * C::QPITCH + lane * E;
+      // channels 0 1 2 3 of each four are stored as 1 3 0 2, the order in which the K codes convert
+      if constexpr (E == 2) {
+        const uint32_t two = pack_half2(f[0] * f2, f[1] * f2);
+        __half* d4 = s_q + r * C::QPITCH + (lane >> 1) * 4 + (lane & 1);
+        *reinterpret_cast<uint16_t*>(d4 + 2) = uint16_t(two);
+        *reinterpret_cast<uint16_t*>(d4) = uint16_t(two >> 16);
+      } else {
 #pragma unroll
-      for (int j = 0; j < E; j += 2)
-        *reinterpret_cast<uint32_t*>(dst + j) = pack_half2(f[j] * f2, f[j + 1] * f2);
+        for (int j = 0; j < E; j += 4)
+          *reinterpret_cast<uint2*>(dst + j) =
+              make_uint2(pack_half2(f[j + 1] * f2, f[j + 3] * f2), pack_half2(f[j] * f2, f[j + 2] * f2));
+      }
+      // 256: the K codes convert to code / 256
       if (lane == 0)
-        s_row[r] = make_int4(__float_as_int(r < rows ? a.scale_log2 * __int_as_float((127 - e) << 23) : 0.f), hi, lo, orow);
+        s_row[r] = make_int4(__float_as_int(r < rows ? 256.f * a.scale_log2 * __int_as_float((127 - e) << 23) : 0.f), hi, lo, orow);
     }
     __syncthreads();
-
-    const int i0 = int(int64_t(tile) * ROWS / a.group), i1 = int((int64_t(tile) * ROWS + rows - 1) / a.group);
-    const int hi_all = a.b.hi(x.pos0 + i0, x.len), hi_any = a.b.hi(x.pos0 + i1, x.len);
-    const int lo_any = a.b.lo(x.pos0 + i0), lo_all = a.b.lo(x.pos0 + i1);
 
     uint32_t qf[kQRegs ? NG * KI * 8 : 1];
     const uint32_t qaddr = base + C::OFF_Q + g * (C::QPITCH * 2) + t * 32;
@@ -296,72 +388,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
       fac[n][1] = __int_as_float(s_row[8 * n + 2 * t + 1].x);
     }
 
-    // ---- the warp's steps: i-th is step c0 kWarps + warp + i kWarps of the unit ----
-    const int count = c1 - c0;
-    // meta of step i: first key (-1: skip), page (-1: outside the cache, zeros), scales
-    auto load_meta = [&](int i) {                 // 32 steps from i on, one per lane
-      const int st = (c0 + i + lane) * kWarps + warp;
-      int key = -1, pg = -1;
-      float ks = 0.f, vs = 0.f;
-      if (i + lane < count && st < x.steps) {
-        int page, inner;
-        if (a.selected) {
-          const int j = st >> (a.b.page_shift - 4);
-          page = __ldg(a.selected + (int64_t(x.tok0) * a.hkv + h) * a.n_selected + j);
-          inner = (st << 4) & (ps - 1);
-        } else {
-          const int kk = x.key0 + st * kStep;
-          page = kk >> a.b.page_shift;
-          inner = kk & (ps - 1);
-        }
-        if (unsigned(page) < unsigned(a.b.max_pages)) {
-          key = (page << a.b.page_shift) + inner;
-          if (key >= hi_any || key + kStep <= lo_any) {
-            key = -1;
-          } else {
-            pg = __ldg(a.b.page_table + int64_t(x.b) * a.b.max_pages + page);
-            if (unsigned(pg) < unsigned(a.num_pages)) {
-              ks = __ldg(a.k_scale + int64_t(pg) * a.hkv + h);
-              vs = __ldg(a.v_scale + int64_t(pg) * a.hkv + h);
-            } else {
-              pg = -1;
-            }
-          }
-        }
-      }
-      s_meta[(i + lane) & 63] = make_int4(key, pg, __float_as_int(ks), __float_as_int(vs));
-      __syncwarp();
-    };
-    auto issue = [&](int i) {
-      if (i < count) {
-        if ((i & 31) == 0) load_meta(i);
-        const int4 m = s_meta[i & 63];
-        if (m.x >= 0) {
-          const int bytes = m.y >= 0 ? 16 : 0;
-          const int64_t o = ((int64_t(max(m.y, 0)) * a.hkv + h) << a.b.page_shift) + (m.x & (ps - 1));
-          const uint8_t* kp = a.k + o * D + g * D + t * 16;
-          const uint8_t* vp = a.v + o * D + 2 * t * D + g * C::VB;
-          const uint32_t st = uint32_t(i % S) * C::STAGE_BYTES;
-#pragma unroll
-          for (int j = 0; j < KI; ++j) {
-            cp16(ring + st + (2 * j) * 512, kp + j * 64, bytes);
-            cp16(ring + st + (2 * j + 1) * 512, kp + 8 * D + j * 64, bytes);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {           // keys 2t, 2t+1, 2t+8, 2t+9
-            const uint8_t* p = vp + ((j & 1) + (j >> 1) * 8) * D;
-            if constexpr (D == 64) {
-              cp8(ring_v8 + st + KI * 1024 + j * 256, p, bytes >> 1);
-            } else {
-#pragma unroll
-              for (int v = 0; v < C::VB / 16; ++v) cp16(ring + st + KI * 1024 + (j * (C::VB / 16) + v) * 512, p + v * 16, bytes);
-            }
-          }
-        }
-      }
-      cp_commit();
-    };
-
     float o[D / 16][NG][4];
     float m[NG][2], l[NG][2];
 #pragma unroll
@@ -371,15 +397,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.f;
     }
-#pragma unroll
-    for (int i = 0; i < S - 1; ++i) issue(i);
-
     for (int i = 0; i < count; ++i) {
+      cp_wait<S - 2>();                           // this lane's copies of step i are there,
+      __syncwarp();                               // every lane's are, and step i - 1 has been read
       issue(i + S - 1);
-      cp_wait<S - 1>();                           // this lane's bytes of step i are there
-      const int4 meta = s_meta[i & 63];
-      const int key = meta.x;
+      const int key = s_meta[i & 63].x;
       if (key < 0) continue;
+      const float2 scale = s_scale[i % S];
       const uint32_t st = uint32_t(i % S) * C::STAGE_BYTES;
 
       // S^T = K Q^T
@@ -388,15 +412,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
       for (int n = 0; n < NG; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
 #pragma unroll
       for (int j = 0; j < KI; ++j) {
-        const uint4 ka = lds128(ring + st + (2 * j) * 512), kb = lds128(ring + st + (2 * j + 1) * 512);
+        const uint32_t at = (k_at ^ ((j & 1) * 64)) + st + (j >> 1) * 128;
+        const uint4 ka = lds128(at), kb = lds128(at + 8 * D);
         const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
         uint32_t frag[4][4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          frag[c][0] = half2_of_e4m3(wa[c]);
-          frag[c][1] = half2_of_e4m3(wb[c]);
-          frag[c][2] = half2_of_e4m3(wa[c] >> 16);
-          frag[c][3] = half2_of_e4m3(wb[c] >> 16);
+          frag[c][0] = half2_of_odd(wa[c]);
+          frag[c][1] = half2_of_odd(wb[c]);
+          frag[c][2] = half2_of_even(wa[c]);
+          frag[c][3] = half2_of_even(wb[c]);
         }
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
@@ -414,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
       }
 
       // scores in log2 units, masked; accumulator rows are keys key + g and key + g + 8
-      const float ks = __int_as_float(meta.z), vs = __int_as_float(meta.w);
+      const float ks = scale.x, vs = scale.y;
       const bool partial = key + kStep > hi_all || key < lo_all;
       bool over = false;
 #pragma unroll
@@ -469,79 +494,56 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if constexpr (D == 64) {
-          const uint2 w = lds64(ring_v8 + st + KI * 1024 + j * 256);
+          const uint2 w = lds64(v_at + st + ((j & 1) + (j >> 1) * 8) * D);
           vw[j][0] = w.x, vw[j][1] = w.y;
         } else {
 #pragma unroll
           for (int v = 0; v < C::VB / 16; ++v) {
-            const uint4 w = lds128(ring + st + KI * 1024 + (j * (C::VB / 16) + v) * 512);
+            const uint4 w = lds128((v_at ^ ((j & 1) * 64)) + st + ((j & 1) + (j >> 1) * 8) * D + v * 128);
             vw[j][4 * v] = w.x, vw[j][4 * v + 1] = w.y, vw[j][4 * v + 2] = w.z, vw[j][4 * v + 3] = w.w;
           }
         }
       }
       if (partial) {
-        // A code that a row does not see must not reach it even if it is NaN (0 * NaN): codes that no
-        // row of the tile sees become 0; a NaN code that some rows see is taken out and put
-        // into the accumulators of those rows by a second product of indicators.
-        bool nan = false;
+        // a slot behind the request's last token may hold any byte, and 0 * NaN would spread
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int kk = key + 2 * t + (j & 1) + (j >> 1) * 8;
-          const bool dead = kk >= hi_any || kk < lo_any;
+        for (int j = 0; j < 4; ++j)
+          if (key + 2 * t + (j & 1) + (j >> 1) * 8 >= hi_any)
 #pragma unroll
-          for (int w = 0; w < C::VB / 4; ++w) {
-            if (dead) vw[j][w] = 0u;
-            nan |= __vcmpeq4(vw[j][w] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0u;
+            for (int w = 0; w < C::VB / 4; ++w) vw[j][w] = 0u;
+      }
+      if (vs != vs) {                             // a page that holds a NaN: for the rows that see a key of the step
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int4 row = s_row[8 * n + 2 * t + c];
+            if (min(row.y, key + kStep) > max(row.z, key))
+#pragma unroll
+              for (int j = 0; j < D / 16; ++j) o[j][n][c] = o[j][n][c + 2] = vs;
           }
-        }
-        if (__any_sync(~0u, nan)) {
-          uint32_t n0[NG], n1[NG];
-#pragma unroll
-          for (int n = 0; n < NG; ++n) {
-            float see[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int4 row = s_row[8 * n + 2 * t + (c & 1)];
-              const int kk = key + g + 8 * (c >> 1);
-              see[c] = kk < row.y && kk >= row.z ? 1.f : 0.f;
-            }
-            n0[n] = transpose8(pack_half2(see[0], see[1]));
-            n1[n] = transpose8(pack_half2(see[2], see[3]));
-          }
-#pragma unroll
-          for (int w = 0; w < C::VB / 4; ++w) {
-            uint32_t nn[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t is = __vcmpeq4(vw[j][w] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-              nn[j] = is & 0x38383838u;           // the code of 1
-              vw[j][w] &= ~is;
-            }
-            const uint32_t a01 = __byte_perm(nn[0], nn[1], 0x5140), a23 = __byte_perm(nn[0], nn[1], 0x7362);
-            const uint32_t b01 = __byte_perm(nn[2], nn[3], 0x5140), b23 = __byte_perm(nn[2], nn[3], 0x7362);
-            const uint32_t f0[4] = {half2_of_e4m3(a01), half2_of_e4m3(a01 >> 16), half2_of_e4m3(b01), half2_of_e4m3(b01 >> 16)};
-            const uint32_t f1[4] = {half2_of_e4m3(a23), half2_of_e4m3(a23 >> 16), half2_of_e4m3(b23), half2_of_e4m3(b23 >> 16)};
-#pragma unroll
-            for (int n = 0; n < NG; ++n) {
-              float x0[4] = {0.f, 0.f, 0.f, 0.f}, x1[4] = {0.f, 0.f, 0.f, 0.f};
-              mma(x0, f0, n0[n], n1[n]);
-              mma(x1, f1, n0[n], n1[n]);
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                if (x0[c] > 0.f) o[2 * w][n][c] = __int_as_float(0x7fffffff);
-                if (x1[c] > 0.f) o[2 * w + 1][n][c] = __int_as_float(0x7fffffff);
-              }
-            }
-          }
-        }
+        continue;
       }
 #pragma unroll
       for (int w = 0; w < C::VB / 4; ++w) {
-        // bytes 4w .. 4w+3 of the lane's channels: rows g and g + 8 of tiles 2w and 2w + 1
-        const uint32_t a01 = __byte_perm(vw[0][w], vw[1][w], 0x5140), a23 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
-        const uint32_t b01 = __byte_perm(vw[2][w], vw[3][w], 0x5140), b23 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
-        const uint32_t f0[4] = {half2_of_e4m3(a01), half2_of_e4m3(a01 >> 16), half2_of_e4m3(b01), half2_of_e4m3(b01 >> 16)};
-        const uint32_t f1[4] = {half2_of_e4m3(a23), half2_of_e4m3(a23 >> 16), half2_of_e4m3(b23), half2_of_e4m3(b23 >> 16)};
+        // bytes 4w .. 4w+3 of the lane's channels: rows g and g + 8 of tiles 2w and 2w + 1. Every other
+        // word converts on the XU pipe, which is idle otherwise.
+        uint32_t f0[4], f1[4];
+        const bool xu = w & 1;
+        const float vw_scale = xu ? vs * (1.f / 256.f) : vs;   // the accumulators hold out / 256
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {             // keys 2t, 2t+1, then 2t+8, 2t+9
+          const uint32_t lo = vw[2 * j][w], hi = vw[2 * j + 1][w];
+          if (xu) {
+            const uint32_t c01 = __byte_perm(lo, hi, 0x5140), c23 = __byte_perm(lo, hi, 0x7362);
+            f0[2 * j] = half2_of_e4m3(c01), f0[2 * j + 1] = half2_of_e4m3(c01 >> 16);
+            f1[2 * j] = half2_of_e4m3(c23), f1[2 * j + 1] = half2_of_e4m3(c23 >> 16);
+          } else {
+            const uint32_t c01 = __byte_perm(lo, hi, 0x5410), c23 = __byte_perm(lo, hi, 0x7632);
+            f0[2 * j] = half2_of_even(c01), f0[2 * j + 1] = half2_of_odd(c01);
+            f1[2 * j] = half2_of_even(c23), f1[2 * j + 1] = half2_of_odd(c23);
+          }
+        }
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
           float x0[4] = {0.f, 0.f, 0.f, 0.f}, x1[4] = {0.f, 0.f, 0.f, 0.f};
@@ -549,8 +551,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
           mma(x1, f1, p0[n], p1[n]);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            o[2 * w][n][c] = fmaf(vs, x0[c], o[2 * w][n][c]);
-            o[2 * w + 1][n][c] = fmaf(vs, x1[c], o[2 * w + 1][n][c]);
+            o[2 * w][n][c] = fmaf(vw_scale, x0[c], o[2 * w][n][c]);
+            o[2 * w + 1][n][c] = fmaf(vw_scale, x1[c], o[2 * w + 1][n][c]);
           }
         }
       }
@@ -569,9 +571,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
         y += __shfl_xor_sync(~0u, y, 16);
         const int r = 8 * n + 2 * t + c;
         if (g == 0) s_ml[warp * ROWS + r] = make_float2(m[n][c], y);
-        float* dst = s_o + (warp * ROWS + r) * D + g * C::VB;
+        float* dst = s_o + (warp * ROWS + r) * D + g * (D == 64 ? 8 : 16);
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) *reinterpret_cast<float2*>(dst + 2 * j) = make_float2(o[j][n][c], o[j][n][c + 2]);
+        for (int j = 0; j < D / 16; ++j)          // channels 4w + 2 (j & 1) of the lane, w = j / 2; 16 of each 128
+          *reinterpret_cast<float2*>(dst + (j >> 3) * 128 + (j & 7) * 2) = make_float2(o[j][n][c], o[j][n][c + 2]);
       }
     __syncthreads();
 
@@ -579,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
     const int slot = 2 * blockIdx.x + (line == line0 ? 0 : 1);
     auto finish = [&](int r, int d4, float4 acc, float M, float L) {
       const int orow = s_row[r].w;
-      const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+      const float inv = L > 0.f || L != L ? 256.f / L : 0.f;
       const __nv_bfloat162 lo2 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi2 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
       *reinterpret_cast<uint2*>(a.out + int64_t(orow) * D + d4 * 4) =
           make_uint2(*reinterpret_cast<const uint32_t*>(&lo2), *reinterpret_cast<const uint32_t*>(&hi2));
@@ -612,9 +615,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
       // the last CTA of the item to arrive joins the parts
       const long long item0 = line - c0;
       const int fc = int(cta_of(item0)), lc = int(cta_of(item0 + x.chunks - 1));
-      __threadfence();
       __syncthreads();
       if (tid == 0) {
+        __threadfence();                          // this CTA's part before its arrival
         const uint32_t old = atomicAdd(a.counters + fc, 1u);
         s_last = old == uint32_t(lc - fc);
         if (s_last) a.counters[fc] = 0u;

@@ -84,8 +84,7 @@ __device__ __forceinline__ float2 float2_of_e4m3(uint32_t two) {
   return f;
 }
 
-// Four fp32 -> four e4m3, `a` in the lowest byte: round to nearest even, saturating at +-448,
-// NaN kept.
+// Four fp32 -> four e4m3, `a` in the lowest byte: round to nearest even, saturating at +-448.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   uint16_t lo, hi;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));

@@ -85,18 +85,19 @@ def append(codes, scale, bounds, x, slots, page):
             fin = np.abs(v[np.isfinite(v)])
             need = 2.0 ** scale_exponent(fin.max() if fin.size else 0.0, E4M3_MAX)
             was = scale[pg, h] if off else 0.0
-            now = max(need, was)
-            codes[pg, h, :off] = e4m3_round(codes[pg, h, :off] * (was / now))
-            new = e4m3_round(v / now)
+            nan = np.isnan(v).any() or np.isnan(was)
+            now, ratio = (need, 1.0) if nan else (max(need, was), was / max(need, was))
+            codes[pg, h, :off] = e4m3_round(codes[pg, h, :off] * ratio)
+            new = e4m3_round(np.where(np.isnan(v), 0.0, v) / now)
             codes[pg, h, at] = new
             if bounds is not None:
-                q = np.where(np.isnan(new), 0.0, new) / 4
+                q = new / 4
                 hi, lo = np.ceil(q).max(0), np.floor(q).min(0)
                 if off:
-                    hi = np.maximum(hi, np.ceil(bounds[pg, h, 0] * (was / now)))
-                    lo = np.minimum(lo, np.floor(bounds[pg, h, 1] * (was / now)))
+                    hi = np.maximum(hi, np.ceil(bounds[pg, h, 0] * ratio))
+                    lo = np.minimum(lo, np.floor(bounds[pg, h, 1] * ratio))
                 bounds[pg, h] = np.stack([hi, lo])
-            scale[pg, h] = now
+            scale[pg, h] = np.nan if nan else now
     return codes, scale, bounds
 
 
@@ -141,7 +142,7 @@ def select(q, bounds, k_scale, page_table, rows, page, k, sink, recent, mask="ca
                     unit = 2.0 ** scale_exponent(fin.max() if fin.size else 0.0, 127.0)
                     qi = np.clip(np.round(np.where(np.isnan(x), 0.0, x) / unit), -127, 127)
                     best = max(best, unit * np.where(qi > 0, qi * bounds[pg, h, 0], qi * bounds[pg, h, 1]).sum())
-                sc[p] = 4 * k_scale[pg, h] * best
+                sc[p] = 3.4028234663852886e38 if np.isnan(k_scale[pg, h]) else 4 * k_scale[pg, h] * best
             scores[t, h] = sc.copy()
             sc[:sink] = np.inf
             sc[max(0, have - recent):] = np.inf

@@ -103,8 +103,8 @@ def check_append(cache, k, v, slots, page):
            for c, s, b, x in ((cache.k, cache.k_scale, cache.k_bounds, k), (cache.v, cache.v_scale, None, v))]
     M.attn_kv8_append(cache, k, v, H.i32(slots))
     for (codes, scale, bounds), c, s, b in ((ref[0], cache.k, cache.k_scale, cache.k_bounds), (ref[1], cache.v, cache.v_scale, None)):
-        assert np.array_equal(s.double().cpu().numpy(), scale)
-        np.testing.assert_array_equal(H.values(c), codes)      # NaN equals NaN
+        np.testing.assert_array_equal(s.double().cpu().numpy(), scale)   # NaN equals NaN
+        assert np.array_equal(H.values(c), codes)
         if bounds is not None and b is not None:
             assert np.array_equal(b.cpu().numpy().astype(int), bounds)
 
@@ -319,19 +319,46 @@ def test_unused_slots_and_hidden_keys_may_hold_nan(d):
     v[poison] = 0xFF
     _, _, _, out, lse2, _ = attend(12, lens, qlens, **kw)
     assert torch.equal(out, clean) and torch.equal(lse, lse2)
-    # the third of the four draft tokens writes NaN: the first two rows must not change
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_nan_shows_in_the_rows_that_see_its_page(d):
+    # four draft tokens over a page border: a NaN in the last page's key or value reaches the rows that see
+    # the page, in the heads it was written to, and no other row
+    page, lens, qlens = 32, [66, 40], [4, 1]
+    cache = H.make_cache(d, 10, 2, page, d)
+    table = H.make_table(1, lens, page, 10)
+    plan = M.attn_kv8_plan(hq=4, hkv=2, head_dim=d, page_size=page, mask=masks.causal(), max_q_len=4)
+    q = torch.randn(5, 4, d, generator=torch.Generator().manual_seed(1)).to(bf16).cuda()
+    args = (plan, cache, q, H.i32(table), H.i32(lens), H.i32(H.cu_of(qlens)))
+    k, v = draw_kv(5, 2, 2, d)
+    slots = H.i32([table[0, 2] * page, table[0, 2] * page + 1])
+    M.attn_kv8_append(cache, k, v, slots)
+    clean, lse = M.forward_kv8(*args)
     for x in (k, v):
-        x[table[0, 73 // page], :, 73 % page, ::3] = 0x7F
-    out3, lse3 = M.forward_kv8(M.attn_kv8_plan(hq=4, hkv=2, head_dim=d, page_size=page, mask=masks.causal(), max_q_len=4), cache, q,
-                               H.i32(table), H.i32(lens), H.i32(H.cu_of(qlens)))
-    assert torch.equal(out3[[0, 1, 4]], clean[[0, 1, 4]]) and torch.equal(lse3[[0, 1, 4]], lse[[0, 1, 4]])
-    assert out3[2:4].isnan().all() and lse3[2:4].isnan().all()
-    # NaN values only: the channels that hold them, in the rows that see them
-    k[table[0, 73 // page], :, 73 % page, ::3] = 0x30
-    out4, _ = M.forward_kv8(M.attn_kv8_plan(hq=4, hkv=2, head_dim=d, page_size=page, mask=masks.causal(), max_q_len=4), cache, q,
-                            H.i32(table), H.i32(lens), H.i32(H.cu_of(qlens)))
-    assert torch.equal(out4[[0, 1, 4]], clean[[0, 1, 4]])
-    assert out4[2:4, :, ::3].isnan().all() and out4[2:4, :, 1::3].isfinite().all() and out4[2:4, :, 2::3].isfinite().all()
+        bad = x.clone()
+        bad[1, 1, 7] = float("nan")              # position 65, head 1
+        M.attn_kv8_append(cache, bad if x is k else k, bad if x is v else v, slots)
+        out, l2 = M.forward_kv8(*args)
+        assert torch.equal(out[[0, 1, 4]], clean[[0, 1, 4]]) and torch.equal(l2[[0, 1, 4]], lse[[0, 1, 4]])
+        assert torch.equal(out[2:4, :2], clean[2:4, :2]) and torch.equal(l2[2:4, :2], lse[2:4, :2])
+        assert out[2:4, 2:].isnan().all()
+        assert l2[2:4, 2:].isnan().all() if x is k else torch.equal(l2, lse)
+        ko, vo = (torch.zeros(66, 2, d, dtype=bf16, device="cuda") for _ in range(2))
+        M.attn_kv8_gather(cache, H.i32(table), H.i32([0, 66]), ko, vo)
+        assert (ko if x is k else vo)[64:, 1].isnan().all() and ko[:, 0].isfinite().all() and vo[:64].isfinite().all()
+        M.attn_kv8_append(cache, k, v, slots)    # place 0 again: the page is new
+        out, l2 = M.forward_kv8(*args)
+        assert torch.equal(out, clean) and torch.equal(l2, lse)
+    # a token behind the NaN keeps it; selection puts the page first
+    bad = k.clone()
+    bad[0, 0, 0] = float("nan")
+    middle = H.i32([table[0, 1] * page, table[0, 1] * page + 1])
+    M.attn_kv8_append(cache, bad, v, middle)
+    M.attn_kv8_append(cache, k[1:], v[1:], middle[1:])
+    assert cache.k_scale[table[0, 1], 0].isnan() and cache.k_scale[table[0, 1], 1].isfinite()
+    sel = check_select(cache, q[:1], table[:1], [66], [1], 2, 0, 1, 4, fwd=False)
+    assert sel[0, 0].tolist() == [1, 2]
 
 
 def test_pages_outside_the_cache_read_as_zeros_and_bad_lengths_are_clamped():

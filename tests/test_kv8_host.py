@@ -77,13 +77,15 @@ def cpu_cache(n=4, hkv=2, page=16, d=64):
     """A cache object on the CPU, for the checks that come before the device's."""
     c = kv8.Kv8Cache.__new__(kv8.Kv8Cache)
     c._t = (torch.zeros(n, hkv, page, d, dtype=torch.uint8).view(E4M3),) * 2 + (torch.zeros(n, hkv),) * 2 + (torch.zeros(n, hkv, 2, d, dtype=torch.int8),)
+    kv8._init()
     c._c = kv8.attn_kv8_cache_t(*[t.data_ptr() for t in c._t], n, page, hkv, d)
-    c.num_pages, c.page_size, c.hkv, c.head_dim, c.device = n, page, hkv, d, torch.device("cpu")
+    c._ref = ctypes.byref(c._c)
+    c.num_pages, c.page_size, c.hkv, c.head_dim, c.device, c.index = n, page, hkv, d, torch.device("cpu"), -1
     return c
 
 
 def cpu_plan(hq=4, hkv=2, d=64, page=16):
-    p = kv8.Kv8Plan(None, hq, hkv, d, page, torch.device("cpu"))
+    p = kv8.Kv8Plan(None, hq, hkv, d, page, -1)
     p.handle = ctypes.c_void_p(1)
     p.__class__ = type("P", (kv8.Kv8Plan,), {"__del__": lambda self: None})
     return p
