@@ -10,11 +10,8 @@
 // decode step fill a tile (as the 128-row side of a tcgen05 MMA they would use 6 % of it).
 //
 // What bounds it: HBM. 2 d bytes per key and KV head are read once; at the measured copy rate
-// an SM receives ~23 bytes per clock. The conversion comes next: cvt.f16x2.e4m3x2 measured ~4 clocks
-// of the SM per warp instruction (profiled: the XU pipe 73 % busy at 3.1 TB/s, nothing else above
-// 27 %), which alone caps the stream at 16 bytes per clock. So K and half of V are converted by
-// shifts and logic: the code's sign, exponent and mantissa moved into an fp16 give code / 256,
-// exactly (subnormals too), and the factor goes into the scales.
+// an SM receives ~23 bytes per clock. Next come the issue slots: ~250 instructions of a warp per 16
+// keys of 128 channels (4 KiB), of which 64 convert codes (cvt.f16x2.e4m3x2).
 //
 // Layout. A step is 16 keys (a page holds a whole number of them): 16 d contiguous bytes of K and
 // of V. A warp copies them by cp.async, 512 contiguous bytes per instruction, into its own ring
@@ -26,11 +23,13 @@
 // so that both reads are free of bank conflicts. P passes from the accumulator layout of S^T to
 // the operand layout of P^T by movmatrix.
 //
-// Work. The steps of all (request, KV head, row tile) items form one line, cut into equal
-// parts for the persistent CTAs (each scans the lengths itself); within a CTA the warps take
-// alternate steps of an item and merge in shared memory. An item whose chunks several CTAs share
-// is joined by the last of them to arrive (an atomic counter that it resets), in
-// CTA order, so results do not depend on timing and nothing waits.
+// Work. The keys of all items (request, KV head, row tile), in chunks of kWarps steps, form one line,
+// cut into equal parts for the persistent CTAs, each of which scans the lengths itself. (The rate
+// of the SMs differs by 5 %; cutting items into equal segments handed out by a ticket measured
+// slower at any size: many small ones pay their start and join, few large ones do not divide evenly.)
+// Within an item the warps take alternate steps and merge in shared memory. An item that
+// several CTAs share is joined by the last of them to arrive (an atomic counter that it
+// resets), in the order of the keys: results do not depend on timing, and nothing waits.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -49,6 +48,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 16;                 // keys per step
+constexpr float kNone = -3.402823466e38f;  // running maximum of a row that has seen no key; finite, so differences are never NaN
 constexpr float kLazy = 8.f;              // log2 units a score may exceed the running maximum by
 
 struct FwdArgs {
@@ -80,13 +80,12 @@ struct Cfg {
   static constexpr int STAGE_BYTES = 32 * D;           // 16 keys of K and of V
   static constexpr int RING = kWarps * STAGES * STAGE_BYTES;
   static constexpr int MERGE = kWarps * ROWS * D * 4;
-  static constexpr int QPITCH = D + 8;                 // halves; the pad spreads rows over banks
+  static constexpr bool QREGS = NG * KI <= 4;          // query fragments: at most 32 registers, else shared memory
   static constexpr int OFF_Q = RING > MERGE ? RING : MERGE;
-  static constexpr int OFF_META = OFF_Q + ROWS * QPITCH * 2;
+  static constexpr int OFF_META = OFF_Q + (QREGS ? 0 : NG * KI * 1024);
   static constexpr int OFF_SCALE = OFF_META + kWarps * 64 * 8;    // [warp][stage] k_scale, v_scale
   static constexpr int OFF_ML = OFF_SCALE + kWarps * STAGES * 8;
-  static constexpr int OFF_ROW = OFF_ML + kWarps * ROWS * 8;      // [ROWS] factor, hi, lo, out row
-  static constexpr int SMEM = OFF_ROW + ROWS * 16;
+  static constexpr int SMEM = OFF_ML + kWarps * ROWS * 8;
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return uint32_t(__cvta_generic_to_shared(p)); }
@@ -136,10 +135,15 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// The codes in the odd / even bytes of w as two halves (lower byte first) of code / 256: the
-// sign stays on top, exponent and mantissa move down by one bit (fp16 has a fifth exponent bit).
-__device__ __forceinline__ uint32_t half2_of_odd(uint32_t w) { return (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u); }
-__device__ __forceinline__ uint32_t half2_of_even(uint32_t w) { return ((w << 8) & 0x80008000u) | ((w << 7) & 0x3f803f80u); }
+// (d0, d1) += s (x0, x1) in one instruction
+__device__ __forceinline__ void fma2(float s, float x0, float x1, float& d0, float& d1) {
+  uint64_t a, b, c;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(a) : "f"(s));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(x0), "f"(x1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(d0), "f"(d1));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(c));
+}
 
 // A unit of the work line: a request, or with selected pages a query token.
 struct Unit {
@@ -179,9 +183,8 @@ template <int D, int NG>
 __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(FwdArgs a) {
   using C = Cfg<D, NG>;
   constexpr int ROWS = C::ROWS, KI = C::KI, S = C::STAGES;
-  constexpr bool kQRegs = NG * KI <= 4;           // Q fragments: at most 32 registers, else from shared memory
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ long long s_scan[kWarps], s_found;
+  __shared__ long long s_scan[kWarps], s_off;
   __shared__ int s_unit, s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const uint32_t base = smem_addr(smem);
@@ -189,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
 
   // ---- this CTA's part [line0, line1) of the line of chunks ----
   const int units = a.selected ? a.b.total_q : a.b.batch;
-  auto line_of = [&](const Unit& x) { return (long long)x.chunks * x.tiles * a.hkv; };
+  auto line_of = [&](const Unit& x) { return (long long)x.chunks * (x.tiles * a.hkv); };
   const int per = (units + kThreads - 1) / kThreads, u0 = min(units, tid * per), u1 = min(units, u0 + per);
   long long mine = 0;
   for (int u = u0; u < u1; ++u) mine += line_of(unit_of<ROWS>(a, u));
@@ -200,14 +203,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
   }
   if (lane == 31) s_scan[warp] = inc;
   __syncthreads();
-  long long before = 0, total = 0;
+  long long first = inc - mine, total = 0;        // the line where this thread's units begin
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += s_scan[w];
+    if (w < warp) first += s_scan[w];
     total += s_scan[w];
   }
   const int G = int(min((long long)gridDim.x, total));
   if (int(blockIdx.x) >= G) return;
-  // the first `more` CTAs take part + 1 chunks, the others part
+  // the first `more` CTAs take part + 1 chunks, the others part (64-bit division is slow)
   auto divide = [](long long x, long long y) { return (x | y) >> 31 ? x / y : (long long)(unsigned(x) / unsigned(y)); };
   const long long part = divide(total, G);
   const int more = int(total - part * G);
@@ -217,13 +220,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
     return int(x < wide ? divide(x, part + 1) : more + divide(x - wide, part));
   };
   const long long line0 = start_of(blockIdx.x), line1 = start_of(blockIdx.x + 1);
-  long long first = before + inc - mine;          // the line where this thread's units begin
   if (first <= line0 && line0 < first + mine) {
     for (int u = u0; u < u1; ++u) {
       const long long n = line_of(unit_of<ROWS>(a, u));
       if (line0 < first + n) {
         s_unit = u;
-        s_found = line0 - first;
+        s_off = line0 - first;
         break;
       }
       first += n;
@@ -231,15 +233,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
   }
   __syncthreads();
   int unit = s_unit;
-  long long off = s_found;                        // chunk offset inside the unit
+  long long off = s_off;                          // chunk offset inside the unit
 
-  __half* s_q = reinterpret_cast<__half*>(smem + C::OFF_Q);
   int2* s_meta = reinterpret_cast<int2*>(smem + C::OFF_META) + warp * 64;
   const float2* s_scale = reinterpret_cast<const float2*>(smem + C::OFF_SCALE) + warp * S;
   const uint32_t scale_addr = base + C::OFF_SCALE + warp * (S * 8) + (lane & 1) * 4;
   float2* s_ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
-  int4* s_row = reinterpret_cast<int4*>(smem + C::OFF_ROW);
-  float* s_o = reinterpret_cast<float*>(smem);
+  float2* s_o = reinterpret_cast<float2*>(smem);
   // Chunk c (16 bytes) of a stage's row r lies at chunk c ^ s(r), s(r) = (((r >> 1) & 3) ^ ((r & 1) << 1)) << 1
   // (rows of 64 bytes: c ^ ((r >> 1) & 3)): of the eight lanes of one shared-memory phase, the K reads
   // have two neighbouring rows and four neighbouring chunks, the V reads four rows two apart and two
@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
   const uint32_t copy_to = ring + wr * D + ((D == 64 ? wc ^ ((wr >> 1) & 3) : wc ^ ((((wr >> 1) & 3) ^ ((wr & 1) << 1)) << 1)) << 4);
   const uint32_t k_at = ring + g * D + ((D == 64 ? t ^ ((g >> 1) & 3) : t ^ ((((g >> 1) & 3) ^ ((g & 1) << 1)) << 1)) << 4);
   const uint32_t v_at = ring + 16 * D + 2 * t * D + (D == 64 ? (((g >> 1) ^ t) << 4) + (g & 1) * 8 : (g ^ (t << 1)) << 4);
+  const uint32_t q_at = base + C::OFF_Q + lane * 16;
 
   for (long long line = line0; line < line1;) {
     const Unit x = unit_of<ROWS>(a, unit);
@@ -258,16 +259,30 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
       off = 0;
       continue;
     }
-    const int item = int(off / x.chunks), c0 = int(off - (long long)item * x.chunks);
+    const int item = int(divide(off, x.chunks)), c0 = int(off - (long long)item * x.chunks);
     const int c1 = int(min((long long)x.chunks, c0 + (line1 - line)));
     const int h = item / x.tiles, tile = item - h * x.tiles;
-    const int rows = int(min((long long)ROWS, (long long)x.nq * a.group - (long long)tile * ROWS));
+    const int row0 = tile * ROWS, rows = min(ROWS, x.nq * a.group - row0);
+    const bool whole = c0 == 0 && c1 == x.chunks;
 
     // ---- the warp's steps: the i-th is step (c0 + i) kWarps + warp of the unit ----
-    const int i0 = int(int64_t(tile) * ROWS / a.group), i1 = int((int64_t(tile) * ROWS + rows - 1) / a.group);
+    const int i0 = row0 / a.group, i1 = (row0 + rows - 1) / a.group;
     const int hi_all = a.b.hi(x.pos0 + i0, x.len), hi_any = a.b.hi(x.pos0 + i1, x.len);
     const int lo_any = a.b.lo(x.pos0 + i0), lo_all = a.b.lo(x.pos0 + i1);
     const int count = c1 - c0;
+    // ---- queries: lane (g, t) takes channels 64 i + 16 t + 0 .. 15 of row g of each group, its fragments,
+    // scaled by a power of two per row to below 2^15 in fp16. fac: score factor of rows 2t, 2t + 1
+    // (the loads go before the keys', behind which they would wait)
+    uint4 qw[NG][2 * KI];
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+      const int r = row0 + 8 * n + g;
+      const bool live = 8 * n + g < rows;
+      const int i = live ? r / a.group : 0, head = live ? r - i * a.group : 0;
+      const uint4* q = reinterpret_cast<const uint4*>(a.q + int64_t(x.tok0 + i) * a.q_stride + int64_t(h * a.group + head) * D + 16 * t);
+#pragma unroll
+      for (int j = 0; j < 2 * KI; ++j) qw[n][j] = live ? __ldg(q + (j >> 1) * 8 + (j & 1)) : make_uint4(0, 0, 0, 0);
+    }
     // first key (-1: skip the step) and page (-1: outside the cache, zeros) of the 32 steps from i on
     auto load_meta = [&](int i) {
       const int st = (c0 + i + lane) * kWarps + warp;
@@ -296,6 +311,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
       s_meta[(i + lane) & 63] = make_int2(key, pg);
       __syncwarp();
     };
+    uint32_t put = 0, get = 0;                    // stage that the next copies go to, that the next step is in
     auto issue = [&](int i) {
       if (i < count) {
         if ((i & 31) == 0) load_meta(i);
@@ -306,105 +322,89 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
           const int64_t o = (block << a.b.page_shift) + (m.x & (ps - 1));
           const uint8_t* kp = a.k + o * D + lane * 16;
           const uint8_t* vp = a.v + o * D + lane * 16;
-          const uint32_t st = uint32_t(i % S) * C::STAGE_BYTES;
+          const uint32_t st = put * C::STAGE_BYTES;
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) {      // s() of the rows that the j-th 512 bytes hold
             const uint32_t flip = D == 128 ? (j & 1) * 64 : D == 256 ? (j & 3) * 32 : 0;
             cp16((copy_to ^ flip) + st + j * 512, kp + j * 512, bytes);
             cp16((copy_to ^ flip) + st + 16 * D + j * 512, vp + j * 512, bytes);
           }
-          if (lane < 2) cp4(scale_addr + uint32_t(i % S) * 8, (lane ? a.v_scale : a.k_scale) + block, bytes >> 2);
+          if (lane < 2) cp4(scale_addr + put * 8, (lane ? a.v_scale : a.k_scale) + block, bytes >> 2);
         }
       }
       cp_commit();
+      put = put == S - 1 ? 0 : put + 1;
     };
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) issue(i);
 
-    // ---- rows of the tile: query in fp16, score factor, visible keys ----
-    for (int r = warp; r < ROWS; r += kWarps) {
-      constexpr int E = D / 32;
-      float f[E];
-      unsigned top = 0;
-      int hi = 0, lo = 0, orow = -1;
-#pragma unroll
-      for (int j = 0; j < E; ++j) f[j] = 0.f;
-      if (r < rows) {
-        const int64_t rr = int64_t(tile) * ROWS + r;
-        const int i = int(rr / a.group), head = h * a.group + int(rr - int64_t(i) * a.group);
-        const __nv_bfloat16* q = a.q + int64_t(x.tok0 + i) * a.q_stride + int64_t(head) * D + lane * E;
-        uint32_t w[(E + 1) / 2];
-        if constexpr (E == 2) w[0] = __ldg(reinterpret_cast<const uint32_t*>(q));
-        else if constexpr (E == 4) *reinterpret_cast<uint2*>(w) = __ldg(reinterpret_cast<const uint2*>(q));
-        else *reinterpret_cast<uint4*>(w) = __ldg(reinterpret_cast<const uint4*>(q));
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-          f[j] = __uint_as_float(j & 1 ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
-          top = max(top, (__float_as_uint(f[j]) >> 16) & 0x7fffu);
-        }
-        hi = a.b.hi(x.pos0 + i, x.len);
-        lo = a.b.lo(x.pos0 + i);
-        orow = (x.tok0 + i) * (a.group * a.hkv) + head;
-      }
-      top = __reduce_max_sync(~0u, top);
-      // |q| < 2^(exponent + 1) -> below 2^15; infinities and NaN go through as they are
-      const int e = top >= 0x7f80u ? 0 : min(100, 14 - (int(top >> 7) - 127));
-      const float f2 = __int_as_float((127 + e) << 23);
-      __half* dst = s_q + r * C::QPITCH + lane * E;
-      // channels 0 1 2 3 of each four are stored as 1 3 0 2, the order in which the K codes convert
-      if constexpr (E == 2) {
-        const uint32_t two = pack_half2(f[0] * f2, f[1] * f2);
-        __half* d4 = s_q + r * C::QPITCH + (lane >> 1) * 4 + (lane & 1);
-        *reinterpret_cast<uint16_t*>(d4 + 2) = uint16_t(two);
-        *reinterpret_cast<uint16_t*>(d4) = uint16_t(two >> 16);
-      } else {
-#pragma unroll
-        for (int j = 0; j < E; j += 4)
-          *reinterpret_cast<uint2*>(dst + j) =
-              make_uint2(pack_half2(f[j + 1] * f2, f[j + 3] * f2), pack_half2(f[j] * f2, f[j + 2] * f2));
-      }
-      // 256: the K codes convert to code / 256
-      if (lane == 0)
-        s_row[r] = make_int4(__float_as_int(r < rows ? 256.f * a.scale_log2 * __int_as_float((127 - e) << 23) : 0.f), hi, lo, orow);
-    }
-    __syncthreads();
-
-    uint32_t qf[kQRegs ? NG * KI * 8 : 1];
-    const uint32_t qaddr = base + C::OFF_Q + g * (C::QPITCH * 2) + t * 32;
-    if constexpr (kQRegs) {
-#pragma unroll
-      for (int n = 0; n < NG; ++n)
-#pragma unroll
-        for (int i = 0; i < KI; ++i) {
-          const uint4 q0 = lds128(qaddr + n * (8 * C::QPITCH * 2) + i * 128), q1 = lds128(qaddr + n * (8 * C::QPITCH * 2) + i * 128 + 16);
-          uint32_t* d = qf + (n * KI + i) * 8;
-          d[0] = q0.x, d[1] = q0.y, d[2] = q0.z, d[3] = q0.w, d[4] = q1.x, d[5] = q1.y, d[6] = q1.z, d[7] = q1.w;
-        }
-    }
+    uint32_t qf[C::QREGS ? NG * KI * 8 : 1];
     float fac[NG][2];
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
-      fac[n][0] = __int_as_float(s_row[8 * n + 2 * t].x);
-      fac[n][1] = __int_as_float(s_row[8 * n + 2 * t + 1].x);
+      const bool live = 8 * n + g < rows;
+      unsigned top = 0;
+#pragma unroll
+      for (int j = 0; j < 2 * KI; ++j) {
+        const uint4 w = qw[n][j];
+        const uint32_t v4[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) top = __vmaxu2(top, v4[c] & 0x7fff7fffu);
+      }
+      top = max(top & 0xffffu, top >> 16);
+      top = max(top, __shfl_xor_sync(~0u, top, 1));
+      top = max(top, __shfl_xor_sync(~0u, top, 2));
+      // |q| < 2^(exponent + 1) -> below 2^15; infinities and NaN go through as they are
+      const int e = top >= 0x7f80u ? 0 : min(100, 14 - (int(top >> 7) - 127));
+      const float up = __int_as_float((127 + e) << 23);
+      const float f = live ? a.scale_log2 * __int_as_float((127 - e) << 23) : 0.f;
+      fac[n][0] = __shfl_sync(~0u, f, 8 * t);
+      fac[n][1] = __shfl_sync(~0u, f, 8 * t + 4);
+#pragma unroll
+      for (int j = 0; j < 2 * KI; ++j) {
+        uint32_t d[4];
+        const uint4 w = qw[n][j];
+        const uint32_t v4[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float q0 = __uint_as_float(v4[2 * c] << 16), q1 = __uint_as_float(v4[2 * c] & 0xffff0000u);
+          const float q2 = __uint_as_float(v4[2 * c + 1] << 16), q3 = __uint_as_float(v4[2 * c + 1] & 0xffff0000u);
+          d[2 * c] = pack_half2(q0 * up, q1 * up);
+          d[2 * c + 1] = pack_half2(q2 * up, q3 * up);
+        }
+        if constexpr (C::QREGS) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) qf[(n * 2 * KI + j) * 4 + c] = d[c];
+        } else {                                  // every warp writes the same; a lane reads back its own
+          *reinterpret_cast<uint4*>(smem + C::OFF_Q + (n * 2 * KI + j) * 512 + lane * 16) = make_uint4(d[0], d[1], d[2], d[3]);
+        }
+      }
     }
+    auto sees = [&](int r, int& hi, int& lo) {    // keys of row r of the tile
+      const int i = (row0 + r) / a.group;
+      hi = r < rows ? a.b.hi(x.pos0 + i, x.len) : 0;
+      lo = a.b.lo(x.pos0 + i);
+    };
 
     float o[D / 16][NG][4];
     float m[NG][2], l[NG][2];
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
-      m[n][0] = m[n][1] = -INFINITY;
+      m[n][0] = m[n][1] = kNone;
       l[n][0] = l[n][1] = 0.f;
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.f;
     }
+
     for (int i = 0; i < count; ++i) {
       cp_wait<S - 2>();                           // this lane's copies of step i are there,
       __syncwarp();                               // every lane's are, and step i - 1 has been read
       issue(i + S - 1);
       const int key = s_meta[i & 63].x;
+      const uint32_t st = get * C::STAGE_BYTES;
+      const float2 scale = s_scale[get];
+      get = get == S - 1 ? 0 : get + 1;
       if (key < 0) continue;
-      const float2 scale = s_scale[i % S];
-      const uint32_t st = uint32_t(i % S) * C::STAGE_BYTES;
 
       // S^T = K Q^T
       float s[NG][4];
@@ -412,25 +412,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
       for (int n = 0; n < NG; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
 #pragma unroll
       for (int j = 0; j < KI; ++j) {
-        const uint32_t at = (k_at ^ ((j & 1) * 64)) + st + (j >> 1) * 128;
-        const uint4 ka = lds128(at), kb = lds128(at + 8 * D);
+        const uint32_t kaddr = (k_at ^ ((j & 1) * 64)) + st + (j >> 1) * 128;
+        const uint4 ka = lds128(kaddr), kb = lds128(kaddr + 8 * D);
         const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
         uint32_t frag[4][4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          frag[c][0] = half2_of_odd(wa[c]);
-          frag[c][1] = half2_of_odd(wb[c]);
-          frag[c][2] = half2_of_even(wa[c]);
-          frag[c][3] = half2_of_even(wb[c]);
+          frag[c][0] = half2_of_e4m3(wa[c]);
+          frag[c][1] = half2_of_e4m3(wb[c]);
+          frag[c][2] = half2_of_e4m3(wa[c] >> 16);
+          frag[c][3] = half2_of_e4m3(wb[c] >> 16);
         }
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
           uint32_t b[8];
-          if constexpr (kQRegs) {
+          if constexpr (C::QREGS) {
 #pragma unroll
             for (int c = 0; c < 8; ++c) b[c] = qf[(n * KI + j) * 8 + c];
           } else {
-            const uint4 q0 = lds128(qaddr + n * (8 * C::QPITCH * 2) + j * 128), q1 = lds128(qaddr + n * (8 * C::QPITCH * 2) + j * 128 + 16);
+            const uint4 q0 = lds128(q_at + (n * KI + j) * 1024), q1 = lds128(q_at + (n * KI + j) * 1024 + 512);
             b[0] = q0.x, b[1] = q0.y, b[2] = q0.z, b[3] = q0.w, b[4] = q1.x, b[5] = q1.y, b[6] = q1.z, b[7] = q1.w;
           }
 #pragma unroll
@@ -448,10 +448,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
         for (int c = 0; c < 4; ++c) s[n][c] *= fac[n][c & 1] * ks;
         if (partial) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int4 row = s_row[8 * n + 2 * t + (c & 1)];
-            const int kk = key + g + 8 * (c >> 1);
-            if (kk >= row.y || kk < row.z) s[n][c] = -INFINITY;
+          for (int c = 0; c < 2; ++c) {
+            int hi, lo;
+            sees(8 * n + 2 * t + c, hi, lo);
+            if (key + g >= hi || key + g < lo) s[n][c] = -INFINITY;
+            if (key + g + 8 >= hi || key + g + 8 < lo) s[n][c + 2] = -INFINITY;
           }
         }
         over |= fmaxf(s[n][0], s[n][2]) > m[n][0] + kLazy || fmaxf(s[n][1], s[n][3]) > m[n][1] + kLazy;
@@ -480,8 +481,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
       uint32_t p0[NG], p1[NG];
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
-        const float ma = m[n][0] == -INFINITY ? 0.f : m[n][0], mb = m[n][1] == -INFINITY ? 0.f : m[n][1];
-        const float e0 = ex2(s[n][0] - ma), e1 = ex2(s[n][1] - mb), e2 = ex2(s[n][2] - ma), e3 = ex2(s[n][3] - mb);
+        const float e0 = ex2(s[n][0] - m[n][0]), e1 = ex2(s[n][1] - m[n][1]);
+        const float e2 = ex2(s[n][2] - m[n][0]), e3 = ex2(s[n][3] - m[n][1]);
         l[n][0] += e0 + e2;
         l[n][1] += e1 + e3;
         p0[n] = transpose8(pack_half2(e0, e1));
@@ -517,8 +518,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
         for (int n = 0; n < NG; ++n)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const int4 row = s_row[8 * n + 2 * t + c];
-            if (min(row.y, key + kStep) > max(row.z, key))
+            int hi, lo;
+            sees(8 * n + 2 * t + c, hi, lo);
+            if (min(hi, key + kStep) > max(lo, key))
 #pragma unroll
               for (int j = 0; j < D / 16; ++j) o[j][n][c] = o[j][n][c + 2] = vs;
           }
@@ -526,23 +528,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
       }
 #pragma unroll
       for (int w = 0; w < C::VB / 4; ++w) {
-        // bytes 4w .. 4w+3 of the lane's channels: rows g and g + 8 of tiles 2w and 2w + 1. Every other
-        // word converts on the XU pipe, which is idle otherwise.
+        // bytes 4w .. 4w+3 of the lane's channels: rows g and g + 8 of tiles 2w and 2w + 1
         uint32_t f0[4], f1[4];
-        const bool xu = w & 1;
-        const float vw_scale = xu ? vs * (1.f / 256.f) : vs;   // the accumulators hold out / 256
 #pragma unroll
         for (int j = 0; j < 2; ++j) {             // keys 2t, 2t+1, then 2t+8, 2t+9
-          const uint32_t lo = vw[2 * j][w], hi = vw[2 * j + 1][w];
-          if (xu) {
-            const uint32_t c01 = __byte_perm(lo, hi, 0x5140), c23 = __byte_perm(lo, hi, 0x7362);
-            f0[2 * j] = half2_of_e4m3(c01), f0[2 * j + 1] = half2_of_e4m3(c01 >> 16);
-            f1[2 * j] = half2_of_e4m3(c23), f1[2 * j + 1] = half2_of_e4m3(c23 >> 16);
-          } else {
-            const uint32_t c01 = __byte_perm(lo, hi, 0x5410), c23 = __byte_perm(lo, hi, 0x7632);
-            f0[2 * j] = half2_of_even(c01), f0[2 * j + 1] = half2_of_odd(c01);
-            f1[2 * j] = half2_of_even(c23), f1[2 * j + 1] = half2_of_odd(c23);
-          }
+          const uint32_t c01 = __byte_perm(vw[2 * j][w], vw[2 * j + 1][w], 0x5140);
+          const uint32_t c23 = __byte_perm(vw[2 * j][w], vw[2 * j + 1][w], 0x7362);
+          f0[2 * j] = half2_of_e4m3(c01), f0[2 * j + 1] = half2_of_e4m3(c01 >> 16);
+          f1[2 * j] = half2_of_e4m3(c23), f1[2 * j + 1] = half2_of_e4m3(c23 >> 16);
         }
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
@@ -550,102 +543,109 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
           mma(x0, f0, p0[n], p1[n]);
           mma(x1, f1, p0[n], p1[n]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            o[2 * w][n][c] = fmaf(vw_scale, x0[c], o[2 * w][n][c]);
-            o[2 * w + 1][n][c] = fmaf(vw_scale, x1[c], o[2 * w + 1][n][c]);
+          for (int c = 0; c < 4; c += 2) {
+            fma2(vs, x0[c], x0[c + 1], o[2 * w][n][c], o[2 * w][n][c + 1]);
+            fma2(vs, x1[c], x1[c + 1], o[2 * w + 1][n][c], o[2 * w + 1][n][c + 1]);
           }
         }
       }
     }
     cp_wait<0>();
 
-    // ---- merge the warps in shared memory (over the ring) ----
+    // ---- merge the warps in shared memory (over the ring). Channel pair p of row r lies at p ^ y, y from
+    // the writing lane's t and g, so that a warp's 8-byte writes take two phases, the least
     __syncthreads();
+    const int y = D == 64 ? t : 2 * t + ((g >> 1) & 1);
 #pragma unroll
     for (int n = 0; n < NG; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float y = l[n][c];
-        y += __shfl_xor_sync(~0u, y, 4);
-        y += __shfl_xor_sync(~0u, y, 8);
-        y += __shfl_xor_sync(~0u, y, 16);
+        float sum = l[n][c];
+        sum += __shfl_xor_sync(~0u, sum, 4);
+        sum += __shfl_xor_sync(~0u, sum, 8);
+        sum += __shfl_xor_sync(~0u, sum, 16);
         const int r = 8 * n + 2 * t + c;
-        if (g == 0) s_ml[warp * ROWS + r] = make_float2(m[n][c], y);
-        float* dst = s_o + (warp * ROWS + r) * D + g * (D == 64 ? 8 : 16);
+        if (g == 0) s_ml[warp * ROWS + r] = make_float2(m[n][c], sum);
+        float2* dst = s_o + (warp * ROWS + r) * (D / 2);
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)          // channels 4w + 2 (j & 1) of the lane, w = j / 2; 16 of each 128
-          *reinterpret_cast<float2*>(dst + (j >> 3) * 128 + (j & 7) * 2) = make_float2(o[j][n][c], o[j][n][c + 2]);
+          dst[(g * (D == 64 ? 4 : 8) + (j >> 3) * 64 + (j & 7)) ^ y] = make_float2(o[j][n][c], o[j][n][c + 2]);
       }
     __syncthreads();
 
-    const bool whole = c0 == 0 && c1 == x.chunks;
-    const int slot = 2 * blockIdx.x + (line == line0 ? 0 : 1);
-    auto finish = [&](int r, int d4, float4 acc, float M, float L) {
-      const int orow = s_row[r].w;
-      const float inv = L > 0.f || L != L ? 256.f / L : 0.f;
+    auto finish = [&](int r, int d4, float4 acc, float M, float Z) {
+      const int i = (row0 + r) / a.group;
+      const int64_t orow = int64_t(x.tok0 + i) * (a.group * a.hkv) + h * a.group + (row0 + r - i * a.group);
+      const float inv = Z > 0.f || Z != Z ? 1.f / Z : 0.f;
       const __nv_bfloat162 lo2 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi2 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-      *reinterpret_cast<uint2*>(a.out + int64_t(orow) * D + d4 * 4) =
+      *reinterpret_cast<uint2*>(a.out + orow * D + d4 * 4) =
           make_uint2(*reinterpret_cast<const uint32_t*>(&lo2), *reinterpret_cast<const uint32_t*>(&hi2));
-      if (a.lse && d4 == 0) a.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+      if (a.lse && d4 == 0) a.lse[orow] = Z == 0.f ? -INFINITY : (M + log2f(Z)) * 0.6931471805599453f;
     };
     for (int idx = tid; idx < rows * (D / 4); idx += kThreads) {
       const int r = idx / (D / 4), d4 = idx % (D / 4);
-      float M = -INFINITY;
+      const int gg = D == 64 ? 0 : (d4 >> 2) & 7, yy = D == 64 ? (r >> 1) & 3 : 2 * ((r >> 1) & 3) + ((gg >> 1) & 1);
+      float M = kNone;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * ROWS + r].x);
-      const float Ms = M == -INFINITY ? 0.f : M;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      float L = 0.f;
+      float Z = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float2 ml = s_ml[w * ROWS + r];
-        const float e = ex2(ml.x - Ms);
-        const float4 y = *reinterpret_cast<const float4*>(s_o + (w * ROWS + r) * D + d4 * 4);
-        L = fmaf(e, ml.y, L);
-        acc.x = fmaf(e, y.x, acc.x), acc.y = fmaf(e, y.y, acc.y), acc.z = fmaf(e, y.z, acc.z), acc.w = fmaf(e, y.w, acc.w);
+        const float e = ex2(ml.x - M);
+        const float2* src = s_o + (w * ROWS + r) * (D / 2);
+        const float2 v0 = src[(2 * d4) ^ yy], v1 = src[(2 * d4 + 1) ^ yy];
+        Z = fmaf(e, ml.y, Z);
+        acc.x = fmaf(e, v0.x, acc.x), acc.y = fmaf(e, v0.y, acc.y), acc.z = fmaf(e, v1.x, acc.z), acc.w = fmaf(e, v1.y, acc.w);
       }
       if (whole) {
-        finish(r, d4, acc, M, L);
+        finish(r, d4, acc, M, Z);
       } else {
-        *reinterpret_cast<float4*>(a.part_o + (int64_t(slot) * ROWS + r) * D + d4 * 4) = acc;
-        if (d4 == 0) *reinterpret_cast<float2*>(a.part_ml + (int64_t(slot) * ROWS + r) * 2) = make_float2(M, L);
+        // a CTA has at most two parts of items: one at the start of its line, one at the end
+        const int64_t slot = 2 * blockIdx.x + (line == line0 ? 0 : 1);
+        __stcg(reinterpret_cast<float4*>(a.part_o + (slot * ROWS + r) * D + d4 * 4), acc);
+        if (d4 == 0) __stcg(reinterpret_cast<float2*>(a.part_ml + (slot * ROWS + r) * 2), make_float2(M, Z));
       }
     }
-    if (!whole) {
-      // the last CTA of the item to arrive joins the parts
+    if (!whole) {                                 // the last CTA of the item to arrive joins the parts
       const long long item0 = line - c0;
-      const int fc = int(cta_of(item0)), lc = int(cta_of(item0 + x.chunks - 1));
+      const int fc = cta_of(item0), n = cta_of(item0 + x.chunks - 1) - fc + 1;
       __syncthreads();
       if (tid == 0) {
         __threadfence();                          // this CTA's part before its arrival
         const uint32_t old = atomicAdd(a.counters + fc, 1u);
-        s_last = old == uint32_t(lc - fc);
+        s_last = old == uint32_t(n - 1);
         if (s_last) a.counters[fc] = 0u;
       }
       __syncthreads();
       if (s_last) {
         __threadfence();
-        const int slot0 = 2 * fc + (start_of(fc) == item0 ? 0 : 1);
+        // parts at slots 2 c, but the first one's where it is not the start of its CTA's line
+        const int odd = start_of(fc) == item0 ? 0 : 1;
+        const float2* pml = reinterpret_cast<const float2*>(a.part_ml) + int64_t(2 * fc) * ROWS;
+        const float4* po = reinterpret_cast<const float4*>(a.part_o + int64_t(2 * fc) * (ROWS * D));
         for (int idx = tid; idx < rows * (D / 4); idx += kThreads) {
-          const int r = idx / (D / 4), d4 = idx % (D / 4);
-          float M = -INFINITY, L = 0.f;
+          const int r = idx / (D / 4);
+          float M = kNone, Z = 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int c = fc; c <= lc; ++c) {
-            const int64_t sl = c == fc ? slot0 : 2 * c;
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (sl * ROWS + r) * 2));
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(a.part_o + (sl * ROWS + r) * D + d4 * 4));
-            const float Mn = fmaxf(M, ml.x), Ms = Mn == -INFINITY ? 0.f : Mn;
-            const float e0 = ex2(M - Ms), e1 = ex2(ml.x - Ms);
+#pragma unroll 4
+          for (int c = 0; c < n; ++c) {
+            const int slot = c == 0 ? odd : 2 * c;
+            const float2 ml = __ldcg(pml + slot * ROWS + r);
+            const float4 v = __ldcg(po + slot * (ROWS * D / 4) + idx);
+            const float Mn = fmaxf(M, ml.x);
+            const float e0 = ex2(M - Mn), e1 = ex2(ml.x - Mn);
             M = Mn;
-            L = L * e0 + ml.y * e1;
-            acc.x = acc.x * e0 + y.x * e1, acc.y = acc.y * e0 + y.y * e1;
-            acc.z = acc.z * e0 + y.z * e1, acc.w = acc.w * e0 + y.w * e1;
+            Z = Z * e0 + ml.y * e1;
+            acc.x = acc.x * e0 + v.x * e1, acc.y = acc.y * e0 + v.y * e1;
+            acc.z = acc.z * e0 + v.z * e1, acc.w = acc.w * e0 + v.w * e1;
           }
-          finish(r, d4, acc, M, L);
+          finish(r, idx % (D / 4), acc, M, Z);
         }
       }
     }
-    __syncthreads();                              // the next item writes the rows and the ring
+    __syncthreads();                              // the next item writes the ring
     line += c1 - c0;
     off += c1 - c0;
     if (off == unit_chunks) {
