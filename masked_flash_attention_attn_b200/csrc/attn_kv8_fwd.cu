@@ -48,6 +48,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 16;                 // keys per step
+constexpr int kStart = 2;                 // chunks that starting on an item is worth in the line
 constexpr float kNone = -3.402823466e38f;  // running maximum of a row that has seen no key; finite, so differences are never NaN
 constexpr float kLazy = 8.f;              // log2 units a score may exceed the running maximum by
 
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
 
   // ---- this CTA's part [line0, line1) of the line of chunks ----
   const int units = a.selected ? a.b.total_q : a.b.batch;
-  auto line_of = [&](const Unit& x) { return (long long)x.chunks * (x.tiles * a.hkv); };
+  auto line_of = [&](const Unit& x) { return (long long)(x.chunks + kStart) * (x.tiles * a.hkv); };
   const int per = (units + kThreads - 1) / kThreads, u0 = min(units, tid * per), u1 = min(units, u0 + per);
   long long mine = 0;
   for (int u = u0; u < u1; ++u) mine += line_of(unit_of<ROWS>(a, u));
@@ -259,8 +260,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
       off = 0;
       continue;
     }
-    const int item = int(divide(off, x.chunks)), c0 = int(off - (long long)item * x.chunks);
-    const int c1 = int(min((long long)x.chunks, c0 + (line1 - line)));
+    // places 0 .. kStart - 1 of an item stand for its start, the others for its chunks
+    const int length = x.chunks + kStart;
+    const int item = int(divide(off, length)), p0 = int(off - (long long)item * length);
+    const int p1 = int(min((long long)length, p0 + (line1 - line)));
+    const int c0 = max(0, p0 - kStart), c1 = max(0, p1 - kStart);
+    const long long item0 = line - p0;
+    const bool at_start = line == line0;
+    line += p1 - p0;
+    off += p1 - p0;
+    if (c0 == c1) continue;
     const int h = item / x.tiles, tile = item - h * x.tiles;
     const int row0 = tile * ROWS, rows = min(ROWS, x.nq * a.group - row0);
     const bool whole = c0 == 0 && c1 == x.chunks;
@@ -603,14 +612,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
         finish(r, d4, acc, M, Z);
       } else {
         // a CTA has at most two parts of items: one at the start of its line, one at the end
-        const int64_t slot = 2 * blockIdx.x + (line == line0 ? 0 : 1);
+        const int64_t slot = 2 * blockIdx.x + (at_start ? 0 : 1);
         __stcg(reinterpret_cast<float4*>(a.part_o + (slot * ROWS + r) * D + d4 * 4), acc);
         if (d4 == 0) __stcg(reinterpret_cast<float2*>(a.part_ml + (slot * ROWS + r) * 2), make_float2(M, Z));
       }
     }
     if (!whole) {                                 // the last CTA of the item to arrive joins the parts
-      const long long item0 = line - c0;
-      const int fc = cta_of(item0), n = cta_of(item0 + x.chunks - 1) - fc + 1;
+      const int fc = cta_of(item0 + kStart), n = cta_of(item0 + length - 1) - fc + 1;
       __syncthreads();
       if (tid == 0) {
         __threadfence();                          // this CTA's part before its arrival
@@ -622,36 +630,55 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
       if (s_last) {
         __threadfence();
         // parts at slots 2 c, but the first one's where it is not the start of its CTA's line
-        const int odd = start_of(fc) == item0 ? 0 : 1;
+        const int odd = start_of(fc) >= item0 ? 0 : 1;
         const float2* pml = reinterpret_cast<const float2*>(a.part_ml) + int64_t(2 * fc) * ROWS;
         const float4* po = reinterpret_cast<const float4*>(a.part_o + int64_t(2 * fc) * (ROWS * D));
-        for (int idx = tid; idx < rows * (D / 4); idx += kThreads) {
-          const int r = idx / (D / 4);
-          float M = kNone, Z = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int c = 0; c < n; ++c) {
-            const int slot = c == 0 ? odd : 2 * c;
-            const float2 ml = __ldcg(pml + slot * ROWS + r);
-            const float4 v = __ldcg(po + slot * (ROWS * D / 4) + idx);
-            const float Mn = fmaxf(M, ml.x);
-            const float e0 = ex2(M - Mn), e1 = ex2(ml.x - Mn);
-            M = Mn;
-            Z = Z * e0 + ml.y * e1;
-            acc.x = acc.x * e0 + v.x * e1, acc.y = acc.y * e0 + v.y * e1;
-            acc.z = acc.z * e0 + v.z * e1, acc.w = acc.w * e0 + v.w * e1;
+        // the 32 lanes of a warp (D = 64: each 16) hold one row: lane c the weight of part c
+        constexpr int PW = D == 64 ? 16 : 32, N = (ROWS * D / 4 + kThreads - 1) / kThreads;
+        float M[N], Z[N], w[N];
+        float4 acc[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) M[k] = kNone, Z[k] = 0.f, acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int b0 = 0; b0 < n; b0 += PW) {
+          const int mc = b0 + (lane & (PW - 1)), nb = min(PW, n - b0);
+#pragma unroll
+          for (int k = 0; k < N; ++k) {
+            const int r = min(ROWS - 1, (tid + k * kThreads) / (D / 4));
+            float2 ml = make_float2(kNone, 0.f);
+            if (mc < n) ml = __ldcg(pml + (mc == 0 ? odd : 2 * mc) * ROWS + r);
+            float Mn = ml.x;
+#pragma unroll
+            for (int o2 = PW / 2; o2; o2 >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(~0u, Mn, o2));
+            Mn = fmaxf(Mn, M[k]);
+            w[k] = ex2(ml.x - Mn);
+            float zs = w[k] * ml.y;
+#pragma unroll
+            for (int o2 = PW / 2; o2; o2 >>= 1) zs += __shfl_xor_sync(~0u, zs, o2);
+            const float e0 = ex2(M[k] - Mn);
+            M[k] = Mn;
+            Z[k] = fmaf(Z[k], e0, zs);
+            acc[k].x *= e0, acc[k].y *= e0, acc[k].z *= e0, acc[k].w *= e0;
           }
-          finish(r, idx % (D / 4), acc, M, Z);
+#pragma unroll 4
+          for (int c = 0; c < nb; ++c) {
+            const int slot = b0 + c == 0 ? odd : 2 * (b0 + c);
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+              const float4 v = __ldcg(po + slot * (ROWS * D / 4) + min(ROWS * D / 4 - 1, tid + k * kThreads));
+              const float e = __shfl_sync(~0u, w[k], c, PW);
+              acc[k].x = fmaf(e, v.x, acc[k].x), acc[k].y = fmaf(e, v.y, acc[k].y);
+              acc[k].z = fmaf(e, v.z, acc[k].z), acc[k].w = fmaf(e, v.w, acc[k].w);
+            }
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const int idx = tid + k * kThreads;
+          if (idx / (D / 4) < rows) finish(idx / (D / 4), idx % (D / 4), acc[k], M[k], Z[k]);
         }
       }
     }
     __syncthreads();                              // the next item writes the ring
-    line += c1 - c0;
-    off += c1 - c0;
-    if (off == unit_chunks) {
-      ++unit;
-      off = 0;
-    }
   }
 }
 
