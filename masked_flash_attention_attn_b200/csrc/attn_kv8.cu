@@ -40,6 +40,7 @@ __device__ __forceinline__ int find(const int* a, int n, int x) {
 
 __global__ void __launch_bounds__(1024) page_tables_kernel(attn_page_tables_t a, int shift) {
   extern __shared__ int s_prefix[];
+  wait_for_previous_kernel();
   const int B = a.batch;
   int* s_tok = s_prefix;
   int* s_take = s_tok + B + 1;
@@ -192,6 +193,7 @@ __global__ void __launch_bounds__(NT) append_kernel(AppendArgs a) {
   const int t0 = blockIdx.x * a.span, ps = 1 << a.shift, D = a.d, vd = D >> 3;
   const int vshift = 31 - __clz(vd);
   if (tid == 0) s_count = 0;
+  wait_for_previous_kernel();
   __syncthreads();
   if (tid < a.span && t0 + tid < a.tokens) {
     const int t = t0 + tid, s = a.slots[t];
@@ -358,6 +360,7 @@ __global__ void __launch_bounds__(256) gather_kernel(GatherArgs a) {
   __shared__ int s_page[kGatherRows], s_off[kGatherRows];
   const int tid = threadIdx.x;
   const int64_t row0 = int64_t(blockIdx.x) * kGatherRows;
+  wait_for_previous_kernel();
   if (tid < kGatherRows) {
     const int64_t row = row0 + tid;
     int pg = -2, off = 0;         // -2: no row, -1: a page outside the cache
@@ -436,6 +439,7 @@ __global__ void __launch_bounds__(128) page_score_kernel(SelectArgs a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tok = blockIdx.x / a.hkv, h = blockIdx.x - tok * a.hkv;
   const int p0 = blockIdx.y * kScorePages;
+  wait_for_previous_kernel();
   int b, pos, len;
   if (!a.b.token(tok, b, pos, len)) return;
   const int n = (a.b.hi(pos, len) + (1 << a.b.page_shift) - 1) >> a.b.page_shift;
@@ -514,6 +518,7 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(SelectArgs 
   __shared__ int s_hist[256];
   __shared__ int s_digit, s_above;
   __shared__ int s_eq[kSelectThreads / 32], s_gt[kSelectThreads / 32];
+  wait_for_previous_kernel();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tok = blockIdx.x / a.hkv, h = blockIdx.x - tok * a.hkv;
   int b, pos, len;
@@ -622,8 +627,7 @@ attn_status_t attn_page_tables(const attn_page_tables_t* t, attn_stream_t stream
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
     return ATTN_ERR_CUDA;
-  page_tables_kernel<<<grid, threads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(*t, shift);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return launch(page_tables_kernel, dim3(grid), threads, smem, stream, *t, shift);
 }
 
 attn_status_t attn_kv8_append(const attn_kv8_cache_t* c, const void* k_new, int64_t k_stride, const void* v_new,
@@ -657,17 +661,14 @@ attn_status_t attn_kv8_append(const attn_kv8_cache_t* c, const void* k_new, int6
   while (span < c->page_size && int64_t(num_tokens) * c->hkv * 2 >= int64_t(2 * span) * 148 * 16) span *= 2;
   a.span = span;
   const dim3 grid((num_tokens + span - 1) / span, c->hkv, 2);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int vecs = c->page_size * c->head_dim / 8;   // 16-byte vectors of a full page
-  switch (vecs) {
-    case 128: append_kernel<128, 1><<<grid, 128, 0, s>>>(a); break;
-    case 256: append_kernel<128, 2><<<grid, 128, 0, s>>>(a); break;
-    case 512: append_kernel<128, 4><<<grid, 128, 0, s>>>(a); break;
-    case 1024: append_kernel<128, 8><<<grid, 128, 0, s>>>(a); break;
-    case 2048: append_kernel<256, 8><<<grid, 256, 0, s>>>(a); break;
-    default: append_kernel<256, 16><<<grid, 256, 0, s>>>(a); break;
+  switch (c->page_size * c->head_dim / 8) {         // 16-byte vectors of a full page
+    case 128: return launch(append_kernel<128, 1>, grid, 128, 0, stream, a);
+    case 256: return launch(append_kernel<128, 2>, grid, 128, 0, stream, a);
+    case 512: return launch(append_kernel<128, 4>, grid, 128, 0, stream, a);
+    case 1024: return launch(append_kernel<128, 8>, grid, 128, 0, stream, a);
+    case 2048: return launch(append_kernel<256, 8>, grid, 256, 0, stream, a);
+    default: return launch(append_kernel<256, 16>, grid, 256, 0, stream, a);
   }
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 attn_status_t attn_kv8_gather(const attn_kv8_cache_t* c, const int32_t* page_table, int32_t max_pages_per_seq,
@@ -697,8 +698,7 @@ attn_status_t attn_kv8_gather(const attn_kv8_cache_t* c, const int32_t* page_tab
   a.d = c->head_dim;
   a.shift = shift_of(c->page_size);
   const unsigned grid = unsigned((total_k + kGatherRows - 1) / kGatherRows);
-  gather_kernel<<<grid, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return launch(gather_kernel, dim3(grid), 256, 0, stream, a);
 }
 
 attn_status_t attn_kv8_select(const attn_kv8_plan_t* p, const attn_kv8_cache_t* c, const attn_kv8_batch_t* b,
@@ -727,15 +727,13 @@ attn_status_t attn_kv8_select(const attn_kv8_plan_t* p, const attn_kv8_cache_t* 
   a.k = n_selected;
   a.scores = scores;
   a.selected = selected;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const dim3 grid{unsigned(rows), unsigned(chunks)};
   const size_t smem = size_t(a.group) * (2 * p->d + 4);
-  if (p->d == 64) page_score_kernel<64><<<grid, 128, smem, s>>>(a);
-  else if (p->d == 128) page_score_kernel<128><<<grid, 128, smem, s>>>(a);
-  else page_score_kernel<256><<<grid, 128, smem, s>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-  page_select_kernel<<<unsigned(rows), kSelectThreads, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  const attn_status_t scored = p->d == 64    ? launch(page_score_kernel<64>, grid, 128, smem, stream, a)
+                               : p->d == 128 ? launch(page_score_kernel<128>, grid, 128, smem, stream, a)
+                                             : launch(page_score_kernel<256>, grid, 128, smem, stream, a);
+  if (scored != ATTN_OK) return scored;
+  return launch(page_select_kernel, dim3(unsigned(rows)), kSelectThreads, 0, stream, a);
 }
 
 }  // extern "C"

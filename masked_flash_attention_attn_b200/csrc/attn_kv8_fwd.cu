@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
   const uint32_t base = smem_addr(smem);
   const int ps = 1 << a.b.page_shift;
 
+  wait_for_previous_kernel();
   // ---- this CTA's part [line0, line1) of the line of chunks ----
   const int units = a.selected ? a.b.total_q : a.b.batch;
   auto line_of = [&](const Unit& x) { return (long long)(x.chunks + kStart) * (x.tiles * a.hkv); };
@@ -805,8 +806,7 @@ attn_status_t attn_kv8_fwd(const attn_kv8_plan_t* p, const attn_kv8_cache_t* c, 
   Kernel k = nullptr;
   int smem = 0, ctas = 0;
   kernel_of(p->d, p->ng, k, smem, ctas);
-  k<<<p->grid, kThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return launch(k, dim3(p->grid), kThreads, smem, stream, a);
 }
 
 }  // extern "C"

@@ -70,6 +70,13 @@ struct Batch {
   }
 };
 
+// Kernels of this cache follow one another in a serving step, each a few microseconds long. They are
+// launched with programmatic stream serialization: a kernel's CTAs may become resident once the
+// CTAs of the kernel before have ended, and this holds them until its writes are visible: select
+// and attend of 4 x 2-8 K tokens 29.9 -> 22.7 us. Letting the next kernel in earlier
+// (griddepcontrol.launch_dependents) measured 30.2: its CTAs take the room of ones that still run.
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // two e4m3 codes (low byte first) -> two halves; exact
 __device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t two) {
   uint32_t r;
@@ -132,6 +139,21 @@ inline attn_status_t check_batch(const attn_kv8_plan_t* p, const attn_kv8_cache_
   if (misaligned(b->q, 16) || misaligned(b->cu_seqlens_q, 4) || misaligned(b->page_table, 4) || misaligned(b->kv_lens, 4))
     return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
+}
+
+template <class... Params, class... Args>
+inline attn_status_t launch(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, attn_stream_t stream, Args... args) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = reinterpret_cast<cudaStream_t>(stream);
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 inline Batch batch_of(const attn_kv8_plan_t* p, const attn_kv8_batch_t* b) {
