@@ -179,8 +179,43 @@ struct AppendArgs {
   int32_t tokens, span, hkv, d, shift, num_slots;
 };
 
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {   // two bf16; a NaN loses
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Four bf16 in two words -> their codes in a unit whose reciprocal inv2 (a power of two, in both
+// halves) is exact, so one rounding
+__device__ __forceinline__ uint32_t codes_of(uint32_t a, uint32_t b, uint32_t inv2) {
+  uint32_t x, y;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(a), "r"(inv2));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(b), "r"(inv2));
+  return e4m3x4(low(x), high(x), low(y), high(y));
+}
+// The rare cases, kept out of the kernel's instruction stream: a unit that a caller chose, and values that are not
+// finite (the largest finite |x| of the word; NaN becomes 0).
+__device__ __noinline__ uint32_t codes_by_division(uint32_t a, uint32_t b, float unit) {
+  return e4m3x4(low(a) / unit, high(a) / unit, low(b) / unit, high(b) / unit);
+}
+__device__ __noinline__ uint32_t without_nan(uint32_t w, unsigned& top) {
+  const unsigned lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
+  if (lo < 0x7f80u) top = max(top, lo);
+  if (hi < 0x7f80u) top = max(top, hi);
+  return (lo > 0x7f80u ? 0u : w & 0xffffu) | (hi > 0x7f80u ? 0u : w & 0xffff0000u);
+}
+
 template <int NT, int NV>
-__global__ void __launch_bounds__(NT) append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(NT, NT == 256 ? 2 : NV <= 4 ? 8 : 5) append_kernel(AppendArgs a) {
+  constexpr int kEnd = -2;        // slot of the tokens before the first and behind the last
+  __shared__ int s_slot[260];     // of the tokens t0 - 1 .. t0 + span + page_size - 1
   __shared__ int s_list[128];
   __shared__ int s_count, s_stop, s_taken[NT / 32];
   __shared__ int2 s_run[128];     // token and place of the run's tokens
@@ -192,77 +227,98 @@ __global__ void __launch_bounds__(NT) append_kernel(AppendArgs a) {
   const int64_t stride = is_v ? a.stride[1] : a.stride[0];
   const int t0 = blockIdx.x * a.span, ps = 1 << a.shift, D = a.d, vd = D >> 3;
   const int vshift = 31 - __clz(vd);
+  auto valid = [&](int s) { return unsigned(s) < unsigned(a.num_slots); };
   if (tid == 0) s_count = 0;
   wait_for_previous_kernel();
+  for (int j = tid; j <= a.span + ps; j += NT) {
+    const int t = t0 - 1 + j;
+    s_slot[j] = t >= 0 && t < a.tokens ? a.slots[t] : kEnd;
+  }
   __syncthreads();
-  if (tid < a.span && t0 + tid < a.tokens) {
-    const int t = t0 + tid, s = a.slots[t];
-    if (unsigned(s) < unsigned(a.num_slots)) {
-      int j = t - 1;              // a run starts where the token before (skipped ones aside) is of another page
-      while (j >= 0 && unsigned(a.slots[j]) >= unsigned(a.num_slots)) --j;
-      if (j < 0 || (a.slots[j] >> a.shift) != (s >> a.shift)) s_list[atomicAdd(&s_count, 1)] = t;
-    }
+  if (tid < a.span && valid(s_slot[tid + 1])) {
+    int before = s_slot[tid];     // a run starts where the token before (skipped ones aside) is of another page
+    for (int t = t0 + tid - 2; t >= 0 && !valid(before); --t) before = a.slots[t];
+    if (!valid(before) || (before >> a.shift) != (s_slot[tid + 1] >> a.shift)) s_list[atomicAdd(&s_count, 1)] = tid;
   }
   __syncthreads();
   const int runs = s_count;
   for (int r = 0; r < runs; ++r) {
-    const int t = s_list[r], pg = a.slots[t] >> a.shift, off = a.slots[t] & (ps - 1);
+    const int j0 = s_list[r] + 1, t = t0 + j0 - 1, s0 = s_slot[j0], pg = s0 >> a.shift, off = s0 & (ps - 1);
     const bool bound = !is_v && a.bounds != nullptr;
     if (bound)
       for (int c = tid; c < D; c += NT) s_hi[c] = -128, s_lo[c] = 127;
-    // the run's tokens, in order: those of the page up to the first of another page
-    int n = 0;
-    for (int w0 = t;; w0 += NT) {
-      if (tid == 0) s_stop = NT;
-      __syncthreads();
-      const int w = w0 + tid, s = w < a.tokens ? a.slots[w] : -1;
-      const bool in = unsigned(s) < unsigned(a.num_slots);
-      if (w >= a.tokens || (in && (s >> a.shift) != pg)) atomicMin(&s_stop, tid);
-      __syncthreads();
-      const int stop = s_stop;
-      const bool take = in && tid < stop;
-      const unsigned m = __ballot_sync(~0u, take);
-      if ((tid & 31) == 0) s_taken[tid >> 5] = __popc(m);
-      __syncthreads();
-      int at = n + __popc(m & ((1u << (tid & 31)) - 1u));
-      for (int i = 0; i < NT / 32; ++i) {
-        if (i < (tid >> 5)) at += s_taken[i];
-        n += s_taken[i];
-      }
-      if (take && at < ps) s_run[at] = make_int2(w, s & (ps - 1));
-      if (stop < NT || n >= ps) break;
-    }
-    n = min(n, ps);
+    if (tid == 0) s_stop = ps - off;
     __syncthreads();
-    const int vecs = n << vshift;
-
-    uint4 x[NV];
-    unsigned top = 0;             // the largest finite |x|, as bf16 bits
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = tid + i * NT;
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (v < vecs)
-        x[i] = *reinterpret_cast<const uint4*>(src + int64_t(s_run[v >> vshift].x) * stride + h * D + (v & (vd - 1)) * 8);
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const unsigned lo = w[j] & 0x7fffu, hi = (w[j] >> 16) & 0x7fffu;
-        if (lo < 0x7f80u) top = max(top, lo);
-        if (hi < 0x7f80u) top = max(top, hi);
-        nan |= lo > 0x7f80u || hi > 0x7f80u;
+    if (tid < ps - off && s_slot[j0 + tid] != s0 + tid) atomicMin(&s_stop, tid);
+    __syncthreads();
+    int n = s_stop;               // tokens in consecutive places
+    const bool whole = n == ps - off || s_slot[j0 + n] == kEnd || (valid(s_slot[j0 + n]) && (s_slot[j0 + n] >> a.shift) != pg);
+    if (!whole) {                 // places or tokens are left out: list the run's tokens, up to the first of another page
+      n = 0;
+      for (int w0 = t;; w0 += NT) {
+        __syncthreads();
+        if (tid == 0) s_stop = NT;
+        __syncthreads();
+        const int w = w0 + tid, s = w < a.tokens ? a.slots[w] : kEnd;
+        if (w >= a.tokens || (valid(s) && (s >> a.shift) != pg)) atomicMin(&s_stop, tid);
+        __syncthreads();
+        const int stop = s_stop;
+        const bool take = valid(s) && tid < stop;
+        const unsigned m = __ballot_sync(~0u, take);
+        if ((tid & 31) == 0) s_taken[tid >> 5] = __popc(m);
+        __syncthreads();
+        int at = n + __popc(m & ((1u << (tid & 31)) - 1u));
+        for (int i = 0; i < NT / 32; ++i) {
+          if (i < (tid >> 5)) at += s_taken[i];
+          n += s_taken[i];
+        }
+        if (take && at < ps) s_run[at] = make_int2(w, s & (ps - 1));
+        if (stop < NT || n >= ps) break;
       }
+      n = min(n, ps);
+      __syncthreads();
     }
-    top = __reduce_max_sync(~0u, top);
-    if ((tid & 31) == 0) s_max[tid >> 5] = top;
-    nan = __syncthreads_or(nan);
-#pragma unroll
-    for (int i = 0; i < NT / 32; ++i) top = max(top, s_max[i]);
+    const int vecs = n << vshift;
+    auto token = [&](int i) { return whole ? t + i : s_run[i].x; };
+    auto place = [&](int i) { return whole ? off + i : s_run[i].y; };
 
     const int64_t block = int64_t(pg) * a.hkv + h;
     float* scale = (is_v ? a.scale[1] : a.scale[0]) + block;
     const float old = off > 0 ? *scale : 0.f;
+    uint4 x[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = tid + i * NT;
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (v < vecs) x[i] = __ldg(reinterpret_cast<const uint4*>(src + int64_t(token(v >> vshift)) * stride + h * D + (v & (vd - 1)) * 8));
+    }
+    unsigned two = 0;             // the largest |x| as bf16 bits, of even and of odd channels
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      two = __vmaxu2(two, __vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu));
+      two = __vmaxu2(two, __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+    }
+    unsigned top = __reduce_max_sync(~0u, max(two & 0xffffu, two >> 16));
+    if ((tid & 31) == 0) s_max[tid >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) top = max(top, s_max[i]);
+    bool nan = top > 0x7f80u;
+    if (top >= 0x7f80u) {         // infinities or NaN among them: the largest finite |x|
+      top = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        x[i].x = without_nan(x[i].x, top), x[i].y = without_nan(x[i].y, top);
+        x[i].z = without_nan(x[i].z, top), x[i].w = without_nan(x[i].w, top);
+      }
+      __syncthreads();
+      top = __reduce_max_sync(~0u, top);
+      if ((tid & 31) == 0) s_max[tid >> 5] = top;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < NT / 32; ++i) top = max(top, s_max[i]);
+    }
+
     // 448 = 1.75 * 2^8: the exponent of top less 8, plus one when its significand is above 1.75
     const int e = max(-126, int(top >> 7) - 127 - 8 + ((top & 127u) > 96u ? 1 : 0));
     nan |= old != old;            // a NaN stays with its page until place 0 is written again
@@ -282,47 +338,48 @@ __global__ void __launch_bounds__(NT) append_kernel(AppendArgs a) {
         *p = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
-    // a power of two has an exact reciprocal; a scale that a caller wrote may be another
+    // a power of two has an exact reciprocal (2^-120 .. 2^126); a scale that a caller wrote may be another
     const bool pow2 = (__float_as_int(now) & 0x7fffff) == 0;
-    const float inv = 1.f / now;
-    int hi8[8], lo8[8];
+    const uint32_t inv = __float_as_uint(1.f / now) >> 16, inv2 = inv | (inv << 16);
+    auto convert = [&](uint32_t p, uint32_t q) { return pow2 ? codes_of(p, q, inv2) : codes_by_division(p, q, now); };
+    // channel-wise extremes of the thread's eight channels (NT is a multiple of vd: the same in every vector)
+    uint32_t hi2[4], lo2[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) hi8[j] = -128, lo8[j] = 127;
+    for (int j = 0; j < 4; ++j) hi2[j] = 0xff80ff80u, lo2[j] = 0x7f807f80u;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = tid + i * NT;
       if (v < vecs) {
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          f[2 * j] = __uint_as_float(w[j] << 16);
-          f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = f[j] != f[j] ? 0.f : pow2 ? f[j] * inv : f[j] / now;
-        const uint32_t c0 = e4m3x4(f[0], f[1], f[2], f[3]), c1 = e4m3x4(f[4], f[5], f[6], f[7]);
-        *reinterpret_cast<uint2*>(codes + s_run[v >> vshift].y * D + (v & (vd - 1)) * 8) = make_uint2(c0, c1);
+        *reinterpret_cast<uint2*>(codes + place(v >> vshift) * D + (v & (vd - 1)) * 8) =
+            make_uint2(convert(x[i].x, x[i].y), convert(x[i].z, x[i].w));
         if (bound) {
-          const uint32_t cc[4] = {c0, c0 >> 16, c1, c1 >> 16};
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 q = float2_of_e4m3(cc[j]);
-            hi8[2 * j] = max(hi8[2 * j], __float2int_ru(q.x * 0.25f));
-            lo8[2 * j] = min(lo8[2 * j], __float2int_rd(q.x * 0.25f));
-            hi8[2 * j + 1] = max(hi8[2 * j + 1], __float2int_ru(q.y * 0.25f));
-            lo8[2 * j + 1] = min(lo8[2 * j + 1], __float2int_rd(q.y * 0.25f));
-          }
+          for (int j = 0; j < 4; ++j) hi2[j] = max2(hi2[j], w[j]), lo2[j] = min2(lo2[j], w[j]);
         }
       }
     }
     if (bound) {
-      if (tid < vecs) {           // NT is a multiple of vd: a thread keeps its eight channels
+      for (int o = vd; o < 32; o <<= 1) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          hi2[j] = max2(hi2[j], __shfl_xor_sync(~0u, hi2[j], o));
+          lo2[j] = min2(lo2[j], __shfl_xor_sync(~0u, lo2[j], o));
+        }
+      }
+      if ((tid & 31) < vd && (tid & ~31) < vecs) {   // rounding is monotone: the extreme's code is the extreme code
         const int c = (tid & (vd - 1)) * 8;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          atomicMax(&s_hi[c + j], hi8[j]);
-          atomicMin(&s_lo[c + j], lo8[j]);
+        for (int j = 0; j < 4; j += 2) {
+          const uint32_t h4 = convert(hi2[j], hi2[j + 1]), l4 = convert(lo2[j], lo2[j + 1]);
+#pragma unroll
+          for (int k = 0; k < 4; k += 2) {
+            const float2 hq = float2_of_e4m3(h4 >> (8 * k)), lq = float2_of_e4m3(l4 >> (8 * k));
+            atomicMax(&s_hi[c + 2 * j + k], __float2int_ru(hq.x * 0.25f));
+            atomicMax(&s_hi[c + 2 * j + k + 1], __float2int_ru(hq.y * 0.25f));
+            atomicMin(&s_lo[c + 2 * j + k], __float2int_rd(lq.x * 0.25f));
+            atomicMin(&s_lo[c + 2 * j + k + 1], __float2int_rd(lq.y * 0.25f));
+          }
         }
       }
       __syncthreads();
