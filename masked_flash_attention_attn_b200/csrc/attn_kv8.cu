@@ -213,7 +213,7 @@ __device__ __noinline__ uint32_t without_nan(uint32_t w, unsigned& top) {
 }
 
 template <int NT, int NV>
-__global__ void __launch_bounds__(NT, NT == 256 ? 2 : NV <= 4 ? 8 : 5) append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(NT, NT == 256 ? 2 : NV <= 4 ? 8 : 7) append_kernel(AppendArgs a) {
   constexpr int kEnd = -2;        // slot of the tokens before the first and behind the last
   __shared__ int s_slot[260];     // of the tokens t0 - 1 .. t0 + span + page_size - 1
   __shared__ int s_list[128];
@@ -501,6 +501,12 @@ __global__ void __launch_bounds__(128) page_score_kernel(SelectArgs a) {
   if (!a.b.token(tok, b, pos, len)) return;
   const int n = (a.b.hi(pos, len) + (1 << a.b.page_shift) - 1) >> a.b.page_shift;
   if (p0 >= n) return;
+  int pages[kScorePages / 32];    // looked up before the queries are quantised
+#pragma unroll
+  for (int r = 0; r < kScorePages / 32; ++r) {
+    const int p = p0 + warp * 8 + (lane >> 2) + 32 * r;
+    pages[r] = p < n ? __ldg(a.b.page_table + int64_t(b) * a.b.max_pages + p) : -1;
+  }
 
   for (int r = warp; r < a.group; r += 4) {
     constexpr int E = D / 32;
@@ -529,24 +535,24 @@ __global__ void __launch_bounds__(128) page_score_kernel(SelectArgs a) {
   }
   __syncthreads();
 
-  const int quad = lane >> 2, t = lane & 3;
-  const int p1 = min(n, p0 + kScorePages);
-  for (int p = p0 + warp * 8 + quad; p < p0 + kScorePages; p += 32) {
-    int pg = -1;
-    if (p < p1) pg = a.b.page_table[int64_t(b) * a.b.max_pages + p];
-    const bool in = unsigned(pg) < unsigned(a.num_pages);
-    const int64_t block = in ? int64_t(pg) * a.hkv + h : 0;
+  // a quad's pages are p0 + 8 warp + quad + 32 r; its lanes share a page's bounds, 64 bytes apart
+  const int t = lane & 3, first = p0 + warp * 8 + (lane >> 2);
+#pragma unroll(D == 256 ? 2 : 4)
+  for (int r = 0; r < kScorePages / 32; ++r) {
+    const int p = first + 32 * r;
+    const bool in = unsigned(pages[r]) < unsigned(a.num_pages);
+    const int64_t block = in ? int64_t(pages[r]) * a.hkv + h : 0;
     uint4 w[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
       w[i] = in ? __ldg(reinterpret_cast<const uint4*>(a.bounds + block * (2 * D)) + 4 * i + t) : make_uint4(0, 0, 0, 0);
     const float ks = in ? __ldg(a.k_scale + block) : 0.f;
     float best = -INFINITY;
-    for (int r = 0; r < a.group; ++r) {
+    for (int q = 0; q < a.group; ++q) {
       int dot = 0;
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const uint4 c = s_q[r * (2 * D / 16) + 4 * i + t];
+        const uint4 c = s_q[q * (2 * D / 16) + 4 * i + t];
         dot = __dp4a(int(w[i].x), int(c.x), dot);
         dot = __dp4a(int(w[i].y), int(c.y), dot);
         dot = __dp4a(int(w[i].z), int(c.z), dot);
@@ -554,9 +560,9 @@ __global__ void __launch_bounds__(128) page_score_kernel(SelectArgs a) {
       }
       dot += __shfl_xor_sync(~0u, dot, 1);
       dot += __shfl_xor_sync(~0u, dot, 2);
-      best = fmaxf(best, float(dot) * s_unit[r]);
+      best = fmaxf(best, float(dot) * s_unit[q]);
     }
-    if (t == 0 && p < p1) {
+    if (t == 0 && p < n) {
       // finite, so that the pages that are always selected stay above it; a page that holds a NaN
       // comes first of the others, so that the NaN shows
       float s = best * (4.f * ks);
@@ -568,15 +574,19 @@ __global__ void __launch_bounds__(128) page_score_kernel(SelectArgs a) {
 
 // The k largest of n scores with ties to the lower page: the k-th largest key by four 8-bit
 // radix passes, then the pages above it and the first of those equal to it, in ascending order.
-// One CTA per token and KV head; the scores come from L2.
+// One CTA per token and KV head. A thread keeps its KEYS keys (0: reads them again in every pass,
+// for rows of any length); scores are alike, so the lanes of a warp that meet in a bin of
+// the leading digits add up first (a bin took a thousand colliding atomics).
 constexpr int kSelectThreads = 512;
 
+template <int KEYS>
 __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(SelectArgs a) {
-  __shared__ int s_hist[256];
-  __shared__ int s_digit, s_above;
-  __shared__ int s_eq[kSelectThreads / 32], s_gt[kSelectThreads / 32];
-  wait_for_previous_kernel();
+  constexpr int W = kSelectThreads / 32;
+  __shared__ int s_hist[4][256];
+  __shared__ int s_eq[2][W], s_gt[2][W];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < 4 * 256; i += kSelectThreads) s_hist[0][i] = 0;
+  wait_for_previous_kernel();
   const int tok = blockIdx.x / a.hkv, h = blockIdx.x - tok * a.hkv;
   int b, pos, len;
   if (!a.b.token(tok, b, pos, len)) return;
@@ -589,64 +599,85 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(SelectArgs 
     for (int i = tid; i < n; i += kSelectThreads) out[i] = i;
     return;
   }
-  auto key = [&](int p) -> uint32_t {
+  auto load = [&](int p) -> uint32_t {            // larger scores have larger keys
     if (p < a.sink || p >= n - a.recent) return 0xffffffffu;
     const uint32_t u = __float_as_uint(scores[p]);
     return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
   };
+  uint32_t keys[KEYS ? KEYS : 1];
+  if constexpr (KEYS > 0) {
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i) keys[i] = tid + i * kSelectThreads < n ? load(tid + i * kSelectThreads) : 0u;
+  }
+  auto each = [&](auto f) {       // f(round, page, key) for every round, by all threads
+    if constexpr (KEYS > 0) {
+#pragma unroll
+      for (int i = 0; i < KEYS; ++i) f(i, tid + i * kSelectThreads, keys[i]);
+    } else {
+      for (int i = 0; i * kSelectThreads < n; ++i) {
+        const int p = tid + i * kSelectThreads;
+        f(i, p, p < n ? load(p) : 0u);
+      }
+    }
+  };
   uint32_t prefix = 0, fixed = 0;
   int rem = a.k;                  // how many of the keys that match the prefix are taken
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) s_hist[tid] = 0;
-    __syncthreads();
-    for (int p = tid; p < n; p += kSelectThreads) {
-      const uint32_t u = key(p);
-      if ((u & fixed) == prefix) atomicAdd(&s_hist[(u >> shift) & 255u], 1);
-    }
-    __syncthreads();
-    if (warp == 0) {              // lane l holds bins 255 - 8 l down to 248 - 8 l
-      int c[8], sum = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum += c[j] = s_hist[255 - 8 * lane - j];
-      int inc = sum;
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(~0u, inc, o);
-        if (lane >= o) inc += x;
+  __syncthreads();
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+    int* hist = s_hist[pass];
+    each([&](int, int p, uint32_t u) {
+      const bool in = p < n && (u & fixed) == prefix;
+      const int digit = in ? int((u >> shift) & 255u) : 256;
+      if (pass < 2) {
+        const unsigned same = __match_any_sync(~0u, digit);
+        if (in && lane == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
+      } else if (in) {
+        atomicAdd(&hist[digit], 1);
       }
-      int above = inc - sum;
-      if (above < rem && inc >= rem) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (above < rem && above + c[j] >= rem) s_digit = 255 - 8 * lane - j, s_above = above;
-          above += c[j];
-        }
-      }
-    }
+    });
     __syncthreads();
-    prefix |= uint32_t(s_digit) << shift;
+    // every warp looks for the digit of the k-th largest: lane l holds bins 255 - 8 l down to 248 - 8 l
+    int c[8], sum = 0, digit = 0, over = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += c[j] = hist[255 - 8 * lane - j];
+    int inc = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(~0u, inc, o);
+      if (lane >= o) inc += x;
+    }
+    int above = inc - sum;
+    const bool mine = above < rem && inc >= rem;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (above < rem && above + c[j] >= rem) digit = 255 - 8 * lane - j, over = above;
+      above += c[j];
+    }
+    const int who = __ffs(__ballot_sync(~0u, mine)) - 1;
+    digit = __shfl_sync(~0u, digit, who);
+    rem -= __shfl_sync(~0u, over, who);
+    prefix |= uint32_t(digit) << shift;
     fixed |= 255u << shift;
-    rem -= s_above;
   }
   int eq0 = 0, gt0 = 0;           // counts before this round's pages
-  for (int base = 0; base < n; base += kSelectThreads) {
-    const int p = base + tid;
-    const uint32_t u = p < n ? key(p) : 0u;
+  each([&](int i, int p, uint32_t u) {
+    if (i * kSelectThreads >= n) return;
     const bool gt = p < n && u > prefix, eq = p < n && u == prefix;
     const unsigned mg = __ballot_sync(~0u, gt), me = __ballot_sync(~0u, eq);
-    if (lane == 0) s_gt[warp] = __popc(mg), s_eq[warp] = __popc(me);
+    if (lane == 0) s_gt[i & 1][warp] = __popc(mg), s_eq[i & 1][warp] = __popc(me);
     __syncthreads();
     int g = gt0, e = eq0;
-    for (int w = 0; w < kSelectThreads / 32; ++w) {
-      if (w < warp) g += s_gt[w], e += s_eq[w];
-      gt0 += s_gt[w];
-      eq0 += s_eq[w];
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const int x = s_gt[i & 1][w], y = s_eq[i & 1][w];
+      if (w < warp) g += x, e += y;
+      gt0 += x, eq0 += y;
     }
     const unsigned below = (1u << lane) - 1u;
     g += __popc(mg & below);
     e += __popc(me & below);
     if (gt || (eq && e < rem)) out[g + min(e, rem)] = p;
-    __syncthreads();
-  }
+  });
 }
 
 }  // namespace
@@ -790,7 +821,10 @@ attn_status_t attn_kv8_select(const attn_kv8_plan_t* p, const attn_kv8_cache_t* 
                                : p->d == 128 ? launch(page_score_kernel<128>, grid, 128, smem, stream, a)
                                              : launch(page_score_kernel<256>, grid, 128, smem, stream, a);
   if (scored != ATTN_OK) return scored;
-  return launch(page_select_kernel, dim3(unsigned(rows)), kSelectThreads, 0, stream, a);
+  const dim3 each{unsigned(rows)};
+  if (b->max_pages_per_seq <= 2 * kSelectThreads) return launch(page_select_kernel<2>, each, kSelectThreads, 0, stream, a);
+  if (b->max_pages_per_seq <= 8 * kSelectThreads) return launch(page_select_kernel<8>, each, kSelectThreads, 0, stream, a);
+  return launch(page_select_kernel<0>, each, kSelectThreads, 0, stream, a);
 }
 
 }  // extern "C"

@@ -495,6 +495,17 @@ def test_select_ties_long_rows_and_special_queries():
     check_select(cache, q, table, lens, [1], 1200, 0, 1, 2, fwd=False)
 
 
+@pytest.mark.parametrize("pages", [1024, 1025, 4096, 4097, 9001])
+def test_select_row_lengths(pages):
+    # around the numbers of keys that the select kernel's threads keep
+    page, d = 16, 64
+    cache = H.make_cache(pages, pages, 1, page, d)
+    table = np.random.default_rng(pages).permutation(pages).astype(np.int32)[None]
+    q = torch.randn(1, 2, d, generator=torch.Generator().manual_seed(2)).to(bf16).cuda()
+    for k in (1, 500):
+        check_select(cache, q, table, [pages * page - 3], [1], k, 0, 1, 2, fwd=False)
+
+
 def test_select_full_mask_sees_every_token():
     cache = H.make_cache(4, 40, 2, 16, 64)
     table = H.make_table(9, [300, 200], 16, 40)
