@@ -23,13 +23,17 @@
 // so that both reads are free of bank conflicts. P passes from the accumulator layout of S^T to
 // the operand layout of P^T by movmatrix.
 //
-// Work. The keys of all items (request, KV head, row tile), in chunks of kWarps steps, form one line,
-// cut into equal parts for the persistent CTAs, each of which scans the lengths itself. (The rate
-// of the SMs differs by 5 %; cutting items into equal segments handed out by a ticket measured
-// slower at any size: many small ones pay their start and join, few large ones do not divide evenly.)
-// Within an item the warps take alternate steps and merge in shared memory. An item that
-// several CTAs share is joined by the last of them to arrive (an atomic counter that it
-// resets), in the order of the keys: results do not depend on timing, and nothing waits.
+// Work. Every persistent CTA scans the lengths itself. The keys of an item (request, KV head, row
+// tile) come in chunks of kWarps steps; within a CTA the warps take alternate steps and merge in
+// shared memory. Two ways to share the chunks out:
+//   one piece each: an item of c chunks is cut into ceil(c / T) equal pieces, T the least tried at
+//     which no more pieces than CTAs are made. Taken when T is within kPiece chunks of the mean.
+//   one line: the chunks of all items in a row (the start of an item counts kStart chunks), cut
+//     evenly, so that a CTA has the end of one item, whole ones, and the start of another.
+// A second piece costs a CTA about 7 chunks (profiled: 32 x 0.5-4 K tokens on a line, CTAs with one
+// piece are done at 28 us, with two at 36). Equal pieces handed out by a ticket measured slower at
+// any size. An item that several CTAs share is joined by the last of them to arrive (an atomic
+// counter that it resets), in the order of the keys: results do not depend on timing, nothing waits.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -45,10 +49,10 @@
 namespace kv8 {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 16;                 // keys per step
 constexpr int kStart = 2;                 // chunks that starting on an item is worth in the line
+constexpr int kPiece = 6;                 // chunks over the mean that one piece each may take
+constexpr int kTries = 8;                 // lengths of a piece that are tried, 1/16 of the mean apart
 constexpr float kNone = -3.402823466e38f;  // running maximum of a row that has seen no key; finite, so differences are never NaN
 constexpr float kLazy = 8.f;              // log2 units a score may exceed the running maximum by
 
@@ -74,19 +78,20 @@ struct FwdArgs {
 template <int D, int NG>
 struct Cfg {
   static constexpr int ROWS = 8 * NG;
+  static constexpr int WARPS = NG == 1 && D <= 128 ? 8 : 4;   // 8: 128 registers and two CTAs per SM
   static constexpr int STAGES = NG >= 4 ? 4 : 3;       // >= NG: the merge overlays the ring
-  static constexpr int CTAS = NG == 1 ? (D == 256 ? 2 : 4) : 2;   // per SM
+  static constexpr int CTAS = 2;                       // per SM
   static constexpr int KI = D / 64;                    // 16-byte K vectors per lane and key
   static constexpr int VB = D / 8;                     // V bytes per lane and key
   static constexpr int STAGE_BYTES = 32 * D;           // 16 keys of K and of V
-  static constexpr int RING = kWarps * STAGES * STAGE_BYTES;
-  static constexpr int MERGE = kWarps * ROWS * D * 4;
+  static constexpr int RING = WARPS * STAGES * STAGE_BYTES;
+  static constexpr int MERGE = WARPS * ROWS * D * 4;
   static constexpr bool QREGS = NG * KI <= 4;          // query fragments: at most 32 registers, else shared memory
   static constexpr int OFF_Q = RING > MERGE ? RING : MERGE;
   static constexpr int OFF_META = OFF_Q + (QREGS ? 0 : NG * KI * 1024);
-  static constexpr int OFF_SCALE = OFF_META + kWarps * 64 * 8;    // [warp][stage] k_scale, v_scale
-  static constexpr int OFF_ML = OFF_SCALE + kWarps * STAGES * 8;
-  static constexpr int SMEM = OFF_ML + kWarps * ROWS * 8;
+  static constexpr int OFF_SCALE = OFF_META + WARPS * 64 * 8;    // [warp][stage] k_scale, v_scale
+  static constexpr int OFF_ML = OFF_SCALE + WARPS * STAGES * 8;
+  static constexpr int SMEM = OFF_ML + WARPS * ROWS * 8;
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return uint32_t(__cvta_generic_to_shared(p)); }
@@ -155,7 +160,7 @@ struct Unit {
   int chunks;       // groups of kWarps steps (at least one, so that empty rows are written)
 };
 
-template <int ROWS>
+template <int ROWS, int WARPS>
 __device__ __forceinline__ Unit unit_of(const FwdArgs& a, int u) {
   Unit x;
   if (a.selected) {
@@ -176,44 +181,81 @@ __device__ __forceinline__ Unit unit_of(const FwdArgs& a, int u) {
     x.steps = hi > lo ? (hi - x.key0 + kStep - 1) / kStep : 0;
   }
   x.tiles = int((int64_t(x.nq) * a.group + ROWS - 1) / ROWS);
-  x.chunks = max(1, (x.steps + kWarps - 1) / kWarps);
+  x.chunks = max(1, (x.steps + WARPS - 1) / WARPS);
   return x;
 }
 
 template <int D, int NG>
-__global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(FwdArgs a) {
+__global__ void __launch_bounds__(32 * Cfg<D, NG>::WARPS, Cfg<D, NG>::CTAS) kv8_fwd_kernel(FwdArgs a) {
   using C = Cfg<D, NG>;
-  constexpr int ROWS = C::ROWS, KI = C::KI, S = C::STAGES;
+  constexpr int ROWS = C::ROWS, KI = C::KI, S = C::STAGES, kWarps = C::WARPS, kThreads = 32 * kWarps;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long s_scan[kWarps], s_off;
+  __shared__ int s_sum[kTries][kWarps];
   __shared__ int s_unit, s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const uint32_t base = smem_addr(smem);
   const int ps = 1 << a.b.page_shift;
 
   wait_for_previous_kernel();
-  // ---- this CTA's part [line0, line1) of the line of chunks ----
+  // ---- this CTA's part [line0, line1) of the line of places (T > 0: pieces, else chunks and starts) ----
   const int units = a.selected ? a.b.total_q : a.b.batch;
-  auto line_of = [&](const Unit& x) { return (long long)(x.chunks + kStart) * (x.tiles * a.hkv); };
   const int per = (units + kThreads - 1) / kThreads, u0 = min(units, tid * per), u1 = min(units, u0 + per);
-  long long mine = 0;
-  for (int u = u0; u < u1; ++u) mine += line_of(unit_of<ROWS>(a, u));
-  long long inc = mine;
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(~0u, inc, o);
-    if (lane >= o) inc += x;
-  }
-  if (lane == 31) s_scan[warp] = inc;
-  __syncthreads();
-  long long first = inc - mine, total = 0;        // the line where this thread's units begin
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) first += s_scan[w];
-    total += s_scan[w];
+  // (64-bit division is slow)
+  auto divide = [](long long x, long long y) { return (x | y) >> 31 ? x / y : (long long)(unsigned(x) / unsigned(y)); };
+  const Unit unit0 = unit_of<ROWS, kWarps>(a, min(u0, units - 1));
+  auto my_unit = [&](int u) { return u == u0 ? unit0 : unit_of<ROWS, kWarps>(a, u); };
+  int T = 0;
+  auto length_of = [&](const Unit& x) { return T ? (x.chunks + T - 1) / T : x.chunks + kStart; };   // places of an item
+  auto line_of = [&](const Unit& x) { return (long long)length_of(x) * (x.tiles * a.hkv); };
+  long long first = 0, mine = 0, total = 0;       // where this thread's units begin in the line, their places
+  auto scan = [&] {
+    mine = 0;
+    for (int u = u0; u < u1; ++u) mine += line_of(my_unit(u));
+    long long inc = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(~0u, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) s_scan[warp] = inc;
+    __syncthreads();
+    first = inc - mine, total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) first += s_scan[w];
+      total += s_scan[w];
+    }
+  };
+  for (int pass = 0;; ++pass) {                   // a loop, so that the scan is there once
+    scan();
+    const int mean = int(min(divide(total, gridDim.x), 0x10000LL));
+    if (pass == 1 || total <= gridDim.x || units > int(gridDim.x) || mean == 0x10000) break;
+    int sum[kTries] = {};                         // pieces at each length
+    for (int u = u0; u < u1; ++u) {
+      const Unit x = my_unit(u);
+      const unsigned items = x.tiles * a.hkv;
+#pragma unroll
+      for (int j = 0; j < kTries; ++j) {
+        const unsigned len = mean + 1 + unsigned(mean) * j / 16;
+        sum[j] += int(min((unsigned long long)items * ((unsigned(x.chunks) + len - 1) / len), 0x100000ull));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kTries; ++j) {
+      sum[j] = __reduce_add_sync(~0u, sum[j]);
+      if (lane == 0) s_sum[j][warp] = sum[j];
+    }
+    __syncthreads();
+    for (int j = kTries - 1; j >= 0; --j) {
+      int pieces = 0;
+      for (int w = 0; w < kWarps; ++w) pieces += s_sum[j][w];
+      const int len = mean + 1 + mean * j / 16;
+      if (pieces <= int(gridDim.x) && len <= mean + kPiece) T = len;
+    }
+    if (T == 0) break;
   }
   const int G = int(min((long long)gridDim.x, total));
   if (int(blockIdx.x) >= G) return;
-  // the first `more` CTAs take part + 1 chunks, the others part (64-bit division is slow)
-  auto divide = [](long long x, long long y) { return (x | y) >> 31 ? x / y : (long long)(unsigned(x) / unsigned(y)); };
+  // the first `more` CTAs take part + 1 places, the others part
   const long long part = divide(total, G);
   const int more = int(total - part * G);
   auto start_of = [&](int c) { return c * part + min(c, more); };
@@ -224,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
   const long long line0 = start_of(blockIdx.x), line1 = start_of(blockIdx.x + 1);
   if (first <= line0 && line0 < first + mine) {
     for (int u = u0; u < u1; ++u) {
-      const long long n = line_of(unit_of<ROWS>(a, u));
+      const long long n = line_of(my_unit(u));
       if (line0 < first + n) {
         s_unit = u;
         s_off = line0 - first;
@@ -254,18 +296,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
   const uint32_t q_at = base + C::OFF_Q + lane * 16;
 
   for (long long line = line0; line < line1;) {
-    const Unit x = unit_of<ROWS>(a, unit);
+    const Unit x = unit_of<ROWS, kWarps>(a, unit);
     const long long unit_chunks = line_of(x);
     if (off >= unit_chunks) {                     // a unit without tokens
       ++unit;
       off = 0;
       continue;
     }
-    // places 0 .. kStart - 1 of an item stand for its start, the others for its chunks
-    const int length = x.chunks + kStart;
+    const int length = length_of(x), lead = T ? 0 : kStart;   // places that stand for the item's start
     const int item = int(divide(off, length)), p0 = int(off - (long long)item * length);
     const int p1 = int(min((long long)length, p0 + (line1 - line)));
-    const int c0 = max(0, p0 - kStart), c1 = max(0, p1 - kStart);
+    const int c0 = T ? int(divide((long long)x.chunks * p0, length)) : max(0, p0 - lead);
+    const int c1 = T ? int(divide((long long)x.chunks * p1, length)) : max(0, p1 - lead);
     const long long item0 = line - p0;
     const bool at_start = line == line0;
     line += p1 - p0;
@@ -619,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
       }
     }
     if (!whole) {                                 // the last CTA of the item to arrive joins the parts
-      const int fc = cta_of(item0 + kStart), n = cta_of(item0 + length - 1) - fc + 1;
+      const int fc = cta_of(item0 + lead), n = cta_of(item0 + length - 1) - fc + 1;
       __syncthreads();
       if (tid == 0) {
         __threadfence();                          // this CTA's part before its arrival
@@ -686,17 +728,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NG>::CTAS) kv8_fwd_kernel(Fwd
 using Kernel = void (*)(FwdArgs);
 
 template <int D, int NG>
-void pick(Kernel& k, int& smem, int& ctas) {
+void pick(Kernel& k, int& smem, int& ctas, int& threads) {
   k = kv8_fwd_kernel<D, NG>;
   smem = Cfg<D, NG>::SMEM;
   ctas = Cfg<D, NG>::CTAS;
+  threads = 32 * Cfg<D, NG>::WARPS;
 }
 
 // head_dim 256: at most 16 rows (the accumulators of 32 would take every register)
-bool kernel_of(int d, int ng, Kernel& k, int& smem, int& ctas) {
-  if (d == 64) ng == 1 ? pick<64, 1>(k, smem, ctas) : ng == 2 ? pick<64, 2>(k, smem, ctas) : pick<64, 4>(k, smem, ctas);
-  else if (d == 128) ng == 1 ? pick<128, 1>(k, smem, ctas) : ng == 2 ? pick<128, 2>(k, smem, ctas) : pick<128, 4>(k, smem, ctas);
-  else ng == 1 ? pick<256, 1>(k, smem, ctas) : pick<256, 2>(k, smem, ctas);
+bool kernel_of(int d, int ng, Kernel& k, int& smem, int& ctas, int& threads) {
+  if (d == 64) ng == 1 ? pick<64, 1>(k, smem, ctas, threads) : ng == 2 ? pick<64, 2>(k, smem, ctas, threads) : pick<64, 4>(k, smem, ctas, threads);
+  else if (d == 128) ng == 1 ? pick<128, 1>(k, smem, ctas, threads) : ng == 2 ? pick<128, 2>(k, smem, ctas, threads) : pick<128, 4>(k, smem, ctas, threads);
+  else ng == 1 ? pick<256, 1>(k, smem, ctas, threads) : pick<256, 2>(k, smem, ctas, threads);
   return k != nullptr;
 }
 
@@ -734,14 +777,14 @@ attn_status_t attn_kv8_plan(const attn_kv8_problem_t* problem, attn_kv8_plan_t**
   const int64_t rows = int64_t(p.hq / p.hkv) * p.max_q_len;
   pl->ng = rows <= 8 ? 1 : rows <= 16 || p.head_dim == 256 ? 2 : 4;
   Kernel k = nullptr;
-  int smem = 0, ctas = 0, sms = 0;
-  kernel_of(pl->d, pl->ng, k, smem, ctas);
+  int smem = 0, ctas = 0, threads = 0, sms = 0;
+  kernel_of(pl->d, pl->ng, k, smem, ctas, threads);
   cudaError_t e = cudaGetDevice(&pl->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, pl->device);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess) {
     int fit = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, k, kThreads, smem);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, k, threads, smem);
     pl->grid = sms * std::max(1, std::min(fit, ctas));
   }
   const size_t tile = size_t(8) * pl->ng, slots = size_t(2) * pl->grid;
@@ -804,9 +847,9 @@ attn_status_t attn_kv8_fwd(const attn_kv8_plan_t* p, const attn_kv8_cache_t* c, 
   a.part_ml = p->part_ml;
   a.counters = p->counters;
   Kernel k = nullptr;
-  int smem = 0, ctas = 0;
-  kernel_of(p->d, p->ng, k, smem, ctas);
-  return launch(k, dim3(p->grid), kThreads, smem, stream, a);
+  int smem = 0, ctas = 0, threads = 0;
+  kernel_of(p->d, p->ng, k, smem, ctas, threads);
+  return launch(k, dim3(p->grid), threads, smem, stream, a);
 }
 
 }  // extern "C"
