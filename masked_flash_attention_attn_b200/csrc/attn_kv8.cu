@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(128) page_score_kernel(SelectArgs a) {
   const int p0 = blockIdx.y * kScorePages;
   wait_for_previous_kernel();
   int b, pos, len;
-  if (!a.b.token(tok, b, pos, len)) return;
+  if (!a.b.token_by_warp(tok, b, pos, len)) return;
   const int n = (a.b.hi(pos, len) + (1 << a.b.page_shift) - 1) >> a.b.page_shift;
   if (p0 >= n) return;
   int pages[kScorePages / 32];    // looked up before the queries are quantised
@@ -541,16 +541,26 @@ __global__ void __launch_bounds__(128) page_score_kernel(SelectArgs a) {
 
   // a quad's pages are p0 + 8 warp + quad + 32 r; its lanes share a page's bounds, 64 bytes apart
   const int t = lane & 3, first = p0 + warp * 8 + (lane >> 2);
-#pragma unroll(D == 256 ? 2 : 4)
-  for (int r = 0; r < kScorePages / 32; ++r) {
-    const int p = first + 32 * r;
-    const bool in = unsigned(pages[r]) < unsigned(a.num_pages);
-    const int64_t block = in ? int64_t(pages[r]) * a.hkv + h : 0;
-    uint4 w[VEC];
+  constexpr int B = 2;            // pages of a quad whose bounds are in flight together
+#pragma unroll
+  for (int r0 = 0; r0 < kScorePages / 32; r0 += B) {
+  uint4 bounds[B][VEC];
+  float scales[B];
+#pragma unroll
+  for (int r = 0; r < B; ++r) {
+    const bool in = unsigned(pages[r0 + r]) < unsigned(a.num_pages);
+    const int64_t block = in ? int64_t(pages[r0 + r]) * a.hkv + h : 0;
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
-      w[i] = in ? __ldg(reinterpret_cast<const uint4*>(a.bounds + block * (2 * D)) + 4 * i + t) : make_uint4(0, 0, 0, 0);
-    const float ks = in ? __ldg(a.k_scale + block) : 0.f;
+      bounds[r][i] = in ? __ldg(reinterpret_cast<const uint4*>(a.bounds + block * (2 * D)) + 4 * i + t) : make_uint4(0, 0, 0, 0);
+    scales[r] = in ? __ldg(a.k_scale + block) : 0.f;
+  }
+#pragma unroll
+  for (int r = 0; r < B; ++r) {
+    const int p = first + 32 * (r0 + r);
+    const bool in = unsigned(pages[r0 + r]) < unsigned(a.num_pages);
+    const uint4 (&w)[VEC] = bounds[r];
+    const float ks = scales[r];
     float best = -INFINITY;
     for (int q = 0; q < a.group; ++q) {
       int dot = 0;
@@ -574,6 +584,7 @@ __global__ void __launch_bounds__(128) page_score_kernel(SelectArgs a) {
       a.scores[(int64_t(tok) * a.hkv + h) * a.b.max_pages + p] = in ? s + 0.f : -INFINITY;
     }
   }
+  }
 }
 
 // The k largest of n scores with ties to the lower page: the k-th largest key by four 8-bit
@@ -593,7 +604,7 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(SelectArgs 
   wait_for_previous_kernel();
   const int tok = blockIdx.x / a.hkv, h = blockIdx.x - tok * a.hkv;
   int b, pos, len;
-  if (!a.b.token(tok, b, pos, len)) return;
+  if (!a.b.token_by_warp(tok, b, pos, len)) return;
   const int n = (a.b.hi(pos, len) + (1 << a.b.page_shift) - 1) >> a.b.page_shift;
   const float* scores = a.scores + (int64_t(tok) * a.hkv + h) * a.b.max_pages;
   int32_t* out = a.selected + (int64_t(tok) * a.hkv + h) * a.k;
