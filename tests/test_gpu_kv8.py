@@ -274,6 +274,77 @@ def test_many_short_requests():
     attend(30, lens, [1] * 700, hq=8, hkv=4, d=64, page=16, sample=500)
 
 
+@pytest.mark.parametrize("d,hq,hkv,page", [(128, 8, 2, 64), (64, 2, 2, 16), (256, 4, 2, 32)])
+@pytest.mark.parametrize("batch,lo,hi", [(3, 9000, 20000), (16, 2000, 3000), (40, 300, 4000), (150, 200, 900), (333, 1, 700)])
+def test_work_is_shared_out_whole(batch, lo, hi, d, hq, hkv, page):
+    # few long items on many CTAs, about one piece per CTA, several items per CTA
+    rng = np.random.default_rng(batch + d)
+    lens = [int(x) for x in rng.integers(lo, hi + 1, batch)]
+    lens[batch // 2] = 0
+    attend(batch + d, lens, [1] * batch, hq=hq, hkv=hkv, d=d, page=page, sample=24)
+
+
+@pytest.mark.parametrize("chunks", [295, 296, 297, 300, 591, 592, 593, 1200])
+def test_work_near_the_number_of_ctas(chunks):
+    # one KV head: the chunks (of 128 keys) of all requests about as many as CTAs
+    lens = [128 * (chunks // 3)] * 2 + [128 * (chunks - 2 * (chunks // 3)) - 60]
+    attend(chunks, lens, [1] * 3, hq=2, hkv=1, d=64, page=128, sample=6)
+
+
+def test_any_scale():
+    # scales that a caller wrote: any positive number
+    cache = H.make_cache(3, 30, 2, 16, 128)
+    g = torch.Generator().manual_seed(2)
+    for s in (cache.k_scale, cache.v_scale):
+        s.mul_(torch.rand(s.shape, generator=g).cuda() + 0.3)
+    attend(6, [400, 37], [2, 1], hq=8, hkv=2, d=128, page=16, cache=cache)
+    before, count = [3, 30], [20, 5]
+    table = H.make_table(2, [a + b for a, b in zip(before, count)], 16, 30)
+    slots = slots_for(table, before, count, 16)
+    k, v = draw_kv(9, len(slots), 2, 128)
+    ref = [O.append(H.values(c), s.double().cpu().numpy(), None, x.float().cpu().numpy(), slots, 16)
+           for c, s, x in ((cache.k, cache.k_scale, k), (cache.v, cache.v_scale, v))]
+    M.attn_kv8_append(cache, k, v, H.i32(slots))
+    for (codes, scale, _), c, s in ((ref[0], cache.k, cache.k_scale), (ref[1], cache.v, cache.v_scale)):
+        assert np.array_equal(s.double().cpu().numpy(), scale)
+        # a quotient is rounded to fp32 before it is rounded to a code: a code next to a tie may be the neighbour
+        got = H.values(c)
+        assert np.mean(got != codes) < 1e-3 and np.all(np.abs(got - codes) <= np.maximum(2.0 ** -9, 2.0 ** -3 * np.abs(codes)))
+
+
+def test_calls_that_are_refused():
+    cache = H.make_cache(1, 8, 2, 16, 64)
+    plan = M.attn_kv8_plan(hq=4, hkv=2, head_dim=64, page_size=16, mask=masks.causal())
+    q = torch.zeros(1, 4, 64, dtype=bf16, device="cuda")
+    table, lens = H.i32([[0, 1]]), H.i32([20])
+    with pytest.raises(M.AttnError, match="INVALID"):
+        M.attn_kv8_fwd(plan, cache, q, table, lens, q)                        # out is q
+    sel, sc = H.i32(np.zeros((1, 2, 3))), torch.zeros(1, 2, 2, device="cuda")
+    for kw in (dict(sink=-1), dict(recent=0), dict(sink=2, recent=2)):
+        with pytest.raises(M.AttnError, match="INVALID"):
+            M.attn_kv8_select(plan, cache, q, table, lens, sc, sel, **kw)
+    window = M.attn_kv8_plan(hq=4, hkv=2, head_dim=64, page_size=16, mask=masks.sliding_window(5))
+    with pytest.raises(M.AttnError, match="UNSUPPORTED"):
+        M.attn_kv8_select(window, cache, q, table, lens, sc, sel)
+    wide = M.attn_kv8_plan(hq=130, hkv=2, head_dim=64, page_size=16, mask=masks.causal())
+    with pytest.raises(M.AttnError, match="UNSUPPORTED"):
+        M.attn_kv8_select(wide, cache, torch.zeros(1, 130, 64, dtype=bf16, device="cuda"), table, lens, sc, sel)
+    with pytest.raises(ValueError, match="cpu"):
+        M.attn_kv8_fwd(plan, cache, q, table.cpu(), lens, torch.empty_like(q))
+    ring = H.i32([0, 1])
+    z = lambda n: H.i32(np.zeros(n))  # noqa: E731
+    good = dict(page_table=table.clone(), old_lens=z(1), new_lens=z(1), free_pages=ring, free_state=z(4), page_size=16, next_state=z(4),
+                kv_lens=z(1), cu_seqlens_q=z(2), slots=z(3))
+    M.attn_page_tables(**good)
+    for name, same in (("next_state", "free_state"), ("kv_lens", "new_lens"), ("kv_lens", "old_lens")):
+        with pytest.raises(M.AttnError, match="INVALID"):
+            M.attn_page_tables(**dict(good, **{name: good[same]}))
+    M.attn_kv8_plan_destroy(plan)
+    M.attn_kv8_plan_destroy(plan)
+    with pytest.raises(ValueError, match="destroyed"):
+        M.attn_kv8_fwd(plan, cache, q, table, lens, torch.empty_like(q))
+
+
 def test_scores_that_rise_along_the_keys_and_wide_scales():
     # every step raises the running maximum; the scales of the pages differ by 2^40
     page, d = 16, 128
@@ -628,6 +699,46 @@ def test_serving_steps_from_a_captured_graph(budget):
         s.launch()
     for want in it:
         assert s.step(want, launch=graph.replay)[2][2] == 0
+
+
+def test_calls_without_tokens_change_nothing():
+    cache = H.make_cache(1, 8, 2, 16, 64)
+    plan = M.attn_kv8_plan(hq=4, hkv=2, head_dim=64, page_size=16, mask=masks.causal())
+    out, lse = M.forward_kv8(plan, cache, torch.zeros(0, 4, 64, dtype=bf16, device="cuda"), H.i32(np.zeros((0, 3))), H.i32([]))
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    # requests, but no query tokens; query rows, but no requests
+    q = torch.ones(3, 4, 64, dtype=bf16, device="cuda")
+    out, lse = torch.full_like(q, 7), torch.full((3, 4), 7.0, device="cuda")
+    M.attn_kv8_fwd(plan, cache, q, H.i32([[0], [1]]), H.i32([5, 9]), out, lse, cu_seqlens_q=H.i32([0, 0, 0]))
+    M.attn_kv8_fwd(plan, cache, q, H.i32(np.zeros((0, 1))), H.i32([]), out, lse, cu_seqlens_q=H.i32([0]))
+    sel, sc = H.i32(np.full((3, 2, 2), 5)), torch.zeros(3, 2, 1, device="cuda")
+    M.attn_kv8_select(plan, cache, q, H.i32([[0], [1]]), H.i32([5, 9]), sc, sel, cu_seqlens_q=H.i32([0, 0, 0]))
+    M.attn_kv8_fwd(plan, cache, q, H.i32([[0], [1]]), H.i32([5, 9]), out, lse, cu_seqlens_q=H.i32([0, 0, 0]), selected=sel)
+    assert (out == 7).all() and (lse == 7).all() and (sel == 5).all()
+
+
+def test_two_captured_graphs_of_two_plans_and_eager_calls_between():
+    # replays of both graphs and eager calls share a cache, each plan has its own workspace
+    lens = [5000, 3000]
+    cache, table, q, out, lse, _ = attend(41, lens, [1, 1], hq=8, hkv=2, d=128, page=16, sample=10)
+    t, n = H.i32(table), H.i32(lens)
+    plans = [M.attn_kv8_plan(hq=8, hkv=2, head_dim=128, page_size=16, mask=masks.causal()) for _ in range(3)]
+    outs, graphs = [torch.empty_like(out) for _ in range(3)], []
+    torch.cuda.synchronize()
+    for p, o in zip(plans[:2], outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            M.attn_kv8_fwd(p, cache, q, t, n, o)
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        M.attn_kv8_fwd(plans[2], cache, q, t, n, outs[2])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, out) for o in outs)
 
 
 def test_two_plans_on_two_streams():
