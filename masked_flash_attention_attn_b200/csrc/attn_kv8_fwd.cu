@@ -50,7 +50,7 @@ namespace kv8 {
 namespace {
 
 constexpr int kStep = 16;                 // keys per step
-constexpr int kStart = 2;                 // chunks that starting on an item is worth in the line
+constexpr int kStart = 3;                 // chunks that starting on an item is worth in the line
 constexpr int kPiece = 6;                 // chunks over the mean that one piece each may take
 constexpr int kTries = 8;                 // lengths of a piece that are tried, 1/16 of the mean apart
 constexpr float kNone = -3.402823466e38f;  // running maximum of a row that has seen no key; finite, so differences are never NaN
