@@ -176,7 +176,7 @@ struct AppendArgs {
   float* scale[2];
   int8_t* bounds;
   const int32_t* slots;
-  int32_t tokens, span, hkv, d, shift, num_slots;
+  int32_t tokens, span, hkv, d, shift, num_slots;   // span: tokens per CTA
 };
 
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {   // two bf16; a NaN loses
@@ -213,7 +213,7 @@ __device__ __noinline__ uint32_t without_nan(uint32_t w, unsigned& top) {
 }
 
 template <int NT, int NV>
-__global__ void __launch_bounds__(NT, NT == 256 ? 2 : NV <= 4 ? 8 : 7) append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(NT, NT == 256 ? 2 : 8) append_kernel(AppendArgs a) {
   constexpr int kEnd = -2;        // slot of the tokens before the first and behind the last
   __shared__ int s_slot[260];     // of the tokens t0 - 1 .. t0 + span + page_size - 1
   __shared__ int s_list[128];
@@ -245,8 +245,6 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NV <= 4 ? 8 : 7) append_ke
   for (int r = 0; r < runs; ++r) {
     const int j0 = s_list[r] + 1, t = t0 + j0 - 1, s0 = s_slot[j0], pg = s0 >> a.shift, off = s0 & (ps - 1);
     const bool bound = !is_v && a.bounds != nullptr;
-    if (bound)
-      for (int c = tid; c < D; c += NT) s_hi[c] = -128, s_lo[c] = 127;
     if (tid == 0) s_stop = ps - off;
     __syncthreads();
     if (tid < ps - off && s_slot[j0 + tid] != s0 + tid) atomicMin(&s_stop, tid);
@@ -279,18 +277,26 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NV <= 4 ? 8 : 7) append_ke
       __syncthreads();
     }
     const int vecs = n << vshift;
-    auto token = [&](int i) { return whole ? t + i : s_run[i].x; };
-    auto place = [&](int i) { return whole ? off + i : s_run[i].y; };
-
+    if (bound)
+      for (int c = tid; c < D; c += NT) s_hi[c] = -128, s_lo[c] = 127;
     const int64_t block = int64_t(pg) * a.hkv + h;
     float* scale = (is_v ? a.scale[1] : a.scale[0]) + block;
     const float old = off > 0 ? *scale : 0.f;
+    // vector v is vector v mod vd of the run's token v / vd; NT is a multiple of vd, so a thread keeps its channels
     uint4 x[NV];
+    const __nv_bfloat16* from = src + h * D + (tid & (vd - 1)) * 8;
+    if (whole) {
+      from += int64_t(t + (tid >> vshift)) * stride;
+      const int64_t step = (NT >> vshift) * stride;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = tid + i * NT;
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (v < vecs) x[i] = __ldg(reinterpret_cast<const uint4*>(src + int64_t(token(v >> vshift)) * stride + h * D + (v & (vd - 1)) * 8));
+      for (int i = 0; i < NV; ++i)
+        x[i] = tid + i * NT < vecs ? __ldg(reinterpret_cast<const uint4*>(from + i * step)) : make_uint4(0, 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int v = tid + i * NT;
+        x[i] = v < vecs ? __ldg(reinterpret_cast<const uint4*>(from + s_run[v >> vshift].x * stride)) : make_uint4(0, 0, 0, 0);
+      }
     }
     unsigned two = 0;             // the largest |x| as bf16 bits, of even and of odd channels
 #pragma unroll
@@ -342,17 +348,29 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NV <= 4 ? 8 : 7) append_ke
     const bool pow2 = (__float_as_int(now) & 0x7fffff) == 0;
     const uint32_t inv = __float_as_uint(1.f / now) >> 16, inv2 = inv | (inv << 16);
     auto convert = [&](uint32_t p, uint32_t q) { return pow2 ? codes_of(p, q, inv2) : codes_by_division(p, q, now); };
-    // channel-wise extremes of the thread's eight channels (NT is a multiple of vd: the same in every vector)
+    if (pow2 && whole) {          // the usual case: one page's codes in a row
+      uint2* to = reinterpret_cast<uint2*>(codes + off * D) + tid;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (tid + i * NT < vecs) to[i * NT] = make_uint2(codes_of(x[i].x, x[i].y, inv2), codes_of(x[i].z, x[i].w, inv2));
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int v = tid + i * NT;
+        if (v < vecs) {
+          const int at = whole ? off * D + v * 8 : s_run[v >> vshift].y * D + (v & (vd - 1)) * 8;
+          *reinterpret_cast<uint2*>(codes + at) = make_uint2(convert(x[i].x, x[i].y), convert(x[i].z, x[i].w));
+        }
+      }
+    }
+    // extremes of the thread's eight channels
     uint32_t hi2[4], lo2[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) hi2[j] = 0xff80ff80u, lo2[j] = 0x7f807f80u;
+    if (bound) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = tid + i * NT;
-      if (v < vecs) {
-        *reinterpret_cast<uint2*>(codes + place(v >> vshift) * D + (v & (vd - 1)) * 8) =
-            make_uint2(convert(x[i].x, x[i].y), convert(x[i].z, x[i].w));
-        if (bound) {
+      for (int i = 0; i < NV; ++i) {
+        if (tid + i * NT < vecs) {
           const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) hi2[j] = max2(hi2[j], w[j]), lo2[j] = min2(lo2[j], w[j]);
@@ -759,9 +777,10 @@ attn_status_t attn_kv8_append(const attn_kv8_cache_t* c, const void* k_new, int6
   a.d = c->head_dim;
   a.shift = shift_of(c->page_size);
   a.num_slots = c->num_pages * c->page_size;
-  // tokens per CTA: enough that the grid is about one wave of 148 x 16 CTAs, at most a page
+  // tokens per CTA: enough that the grid is about one wave of 148 x 16 CTAs, at most half a page (a CTA then has
+  // one run or none: 17.5 us for 13.7 K tokens of 8 x 128 against 18.3 with whole pages, floor 10.2)
   int span = 1;
-  while (span < c->page_size && int64_t(num_tokens) * c->hkv * 2 >= int64_t(2 * span) * 148 * 16) span *= 2;
+  while (2 * span < c->page_size && int64_t(num_tokens) * c->hkv * 2 >= int64_t(2 * span) * 148 * 16) span *= 2;
   a.span = span;
   const dim3 grid((num_tokens + span - 1) / span, c->hkv, 2);
   switch (c->page_size * c->head_dim / 8) {         // 16-byte vectors of a full page
