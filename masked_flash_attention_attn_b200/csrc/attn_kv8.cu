@@ -492,9 +492,10 @@ __global__ void __launch_bounds__(256) gather_kernel(GatherArgs a) {
 
 // ---- page selection -----------------------------------------------------------------------------------
 // Scores. sum_c (qi > 0 ? qi hi_c : qi lo_c) is the dot product of [max(qi, 0), min(qi, 0)] with
-// [hi, lo], so a page costs one pass over its 2 d bound bytes with 4-way int8 dot products. A quad
-// of lanes takes a page (16-byte loads, 64 contiguous bytes per quad), eight pages per warp and
-// step. HBM-bound: 2 d bytes per page and KV head.
+// [hi, lo]: an int8 matrix product of 2 d bound bytes per page with the query heads, on mma.sync
+// m16n8k32 (16 pages, 8 heads). The order of channels is free, so lane (g, t) loads bytes 64 i + 16 t of
+// pages g and g + 8, its operands. HBM-bound: 2 d bytes per page and KV head. (4-way int8 dot
+// products took five times the instructions.)
 constexpr int kScorePages = 128;  // pages per CTA
 constexpr int kMaxGroup = 64;
 
@@ -510,12 +511,22 @@ struct SelectArgs {
   int32_t* selected;
 };
 
+// D += A B, A 16x32 (rows g, g + 8; bytes 4t .. 4t + 3 | 16 more), B 32x8, s8 with s32 accumulators
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 template <int D>
 __global__ void __launch_bounds__(128) page_score_kernel(SelectArgs a) {
-  extern __shared__ uint4 s_q[];  // [group][2 D] int8, then [group] units
+  extern __shared__ uint4 s_q[];  // [heads in eights][2 D] int8, then as many units (-inf: no head)
   constexpr int VEC = D / 32;     // 16-byte vectors per lane and page
-  float* s_unit = reinterpret_cast<float*>(s_q + a.group * (2 * D / 16));
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int ROUNDS = kScorePages / 64;
+  constexpr int PITCH = 2 * D / 16 + 4;   // vectors; neighbouring heads half a line apart: no bank conflicts
+  const int eights = (a.group + 7) >> 3;
+  float* s_unit = reinterpret_cast<float*>(s_q + eights * 8 * PITCH);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int tok = blockIdx.x / a.hkv, h = blockIdx.x - tok * a.hkv;
   const int p0 = blockIdx.y * kScorePages;
   wait_for_previous_kernel();
@@ -523,94 +534,93 @@ __global__ void __launch_bounds__(128) page_score_kernel(SelectArgs a) {
   if (!a.b.token_by_warp(tok, b, pos, len)) return;
   const int n = (a.b.hi(pos, len) + (1 << a.b.page_shift) - 1) >> a.b.page_shift;
   if (p0 >= n) return;
-  int pages[kScorePages / 32];    // looked up before the queries are quantised
+  // the lane's pages are p0 + 64 r + 16 warp + g and 8 more; looked up before the queries are quantised
+  const int first = p0 + 16 * warp + g;
+  int pages[2 * ROUNDS];
 #pragma unroll
-  for (int r = 0; r < kScorePages / 32; ++r) {
-    const int p = p0 + warp * 8 + (lane >> 2) + 32 * r;
+  for (int r = 0; r < 2 * ROUNDS; ++r) {
+    const int p = first + 64 * (r >> 1) + 8 * (r & 1);
     pages[r] = p < n ? __ldg(a.b.page_table + int64_t(b) * a.b.max_pages + p) : -1;
   }
 
-  for (int r = warp; r < a.group; r += 4) {
+  for (int r = warp; r < 8 * eights; r += 4) {
     constexpr int E = D / 32;
-    const __nv_bfloat16* q = a.q + int64_t(tok) * a.q_stride + int64_t(h * a.group + r) * D + lane * E;
+    int8_t* dst = reinterpret_cast<int8_t*>(s_q + r * PITCH) + lane * E;
+    const bool live = r < a.group;
+    const __nv_bfloat16* q = a.q + int64_t(tok) * a.q_stride + int64_t(h * a.group + (live ? r : 0)) * D + lane * E;
     float f[E];
     unsigned top = 0;
 #pragma unroll
     for (int j = 0; j < E; ++j) {
-      f[j] = __bfloat162float(q[j]);
+      f[j] = live ? __bfloat162float(q[j]) : 0.f;
       const unsigned m = (__float_as_uint(f[j]) >> 16) & 0x7fffu;
       if (m < 0x7f80u) top = max(top, m);
     }
     top = __reduce_max_sync(~0u, top);
     // 127 = 1.984375 * 2^6: significand 126 / 128 over 1
     const int e = max(-126, int(top >> 7) - 127 - 6 + ((top & 127u) > 126u ? 1 : 0));
-    int8_t* dst = reinterpret_cast<int8_t*>(s_q) + r * 2 * D + lane * E;
 #pragma unroll
     for (int j = 0; j < E; ++j) {
-      // 2^-e in two factors: e = -126 has a reciprocal, e up to 121 has a normal one
-      const float y = f[j] * __int_as_float((127 - e) << 23);
-      const int qi = min(127, max(-127, __float2int_rn(y)));   // NaN converts to 0
+      const int qi = min(127, max(-127, __float2int_rn(f[j] * __int_as_float((127 - e) << 23))));   // NaN converts to 0
       dst[j] = int8_t(max(qi, 0));
       dst[D + j] = int8_t(min(qi, 0));
     }
-    if (lane == 0) s_unit[r] = __int_as_float((e + 127) << 23);
+    if (lane == 0) s_unit[r] = live ? __int_as_float((e + 127) << 23) : -INFINITY;
   }
   __syncthreads();
 
-  // a quad's pages are p0 + 8 warp + quad + 32 r; its lanes share a page's bounds, 64 bytes apart
-  const int t = lane & 3, first = p0 + warp * 8 + (lane >> 2);
-  constexpr int B = 2;            // pages of a quad whose bounds are in flight together
 #pragma unroll
-  for (int r0 = 0; r0 < kScorePages / 32; r0 += B) {
-  uint4 bounds[B][VEC];
-  float scales[B];
+  for (int r = 0; r < ROUNDS; ++r) {
+    uint4 w[2][VEC];
+    float ks[2], best[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-  for (int r = 0; r < B; ++r) {
-    const bool in = unsigned(pages[r0 + r]) < unsigned(a.num_pages);
-    const int64_t block = in ? int64_t(pages[r0 + r]) * a.hkv + h : 0;
+    for (int z = 0; z < 2; ++z) {
+      const bool in = unsigned(pages[2 * r + z]) < unsigned(a.num_pages);
+      const int64_t block = in ? int64_t(pages[2 * r + z]) * a.hkv + h : 0;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i)
-      bounds[r][i] = in ? __ldg(reinterpret_cast<const uint4*>(a.bounds + block * (2 * D)) + 4 * i + t) : make_uint4(0, 0, 0, 0);
-    scales[r] = in ? __ldg(a.k_scale + block) : 0.f;
-  }
-#pragma unroll
-  for (int r = 0; r < B; ++r) {
-    const int p = first + 32 * (r0 + r);
-    const bool in = unsigned(pages[r0 + r]) < unsigned(a.num_pages);
-    const uint4 (&w)[VEC] = bounds[r];
-    const float ks = scales[r];
-    float best = -INFINITY;
-    for (int q = 0; q < a.group; ++q) {
-      int dot = 0;
+      for (int i = 0; i < VEC; ++i)
+        w[z][i] = in ? __ldg(reinterpret_cast<const uint4*>(a.bounds + block * (2 * D)) + 4 * i + t) : make_uint4(0, 0, 0, 0);
+      ks[z] = in ? __ldg(a.k_scale + block) : 0.f;
+    }
+    for (int e = 0; e < eights; ++e) {
+      int dot[4] = {0, 0, 0, 0};  // pages g, g, g + 8, g + 8 and heads 2t, 2t + 1, 2t, 2t + 1
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const uint4 c = s_q[q * (2 * D / 16) + 4 * i + t];
-        dot = __dp4a(int(w[i].x), int(c.x), dot);
-        dot = __dp4a(int(w[i].y), int(c.y), dot);
-        dot = __dp4a(int(w[i].z), int(c.z), dot);
-        dot = __dp4a(int(w[i].w), int(c.w), dot);
+        const uint4 c = s_q[(8 * e + g) * PITCH + 4 * i + t];
+        mma_s8(dot, w[0][i].x, w[1][i].x, w[0][i].y, w[1][i].y, c.x, c.y);
+        mma_s8(dot, w[0][i].z, w[1][i].z, w[0][i].w, w[1][i].w, c.z, c.w);
       }
-      dot += __shfl_xor_sync(~0u, dot, 1);
-      dot += __shfl_xor_sync(~0u, dot, 2);
-      best = fmaxf(best, float(dot) * s_unit[q]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float unit = s_unit[8 * e + 2 * t + j];
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+          best[z] = fmaxf(best[z], unit > 0.f ? float(dot[2 * z + j]) * unit : -INFINITY);
+      }
     }
-    if (t == 0 && p < n) {
-      // finite, so that the pages that are always selected stay above it; a page that holds a NaN
-      // comes first of the others, so that the NaN shows
-      float s = best * (4.f * ks);
-      s = s != s ? 3.402823466e38f : fminf(fmaxf(s, -3.402823466e38f), 3.402823466e38f);
-      a.scores[(int64_t(tok) * a.hkv + h) * a.b.max_pages + p] = in ? s + 0.f : -INFINITY;
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      best[z] = fmaxf(best[z], __shfl_xor_sync(~0u, best[z], 1));
+      best[z] = fmaxf(best[z], __shfl_xor_sync(~0u, best[z], 2));
+      const int p = first + 64 * r + 8 * z;
+      if (t == 0 && p < n) {
+        // finite, so that the pages that are always selected stay above it; a page that holds a NaN
+        // comes first of the others, so that the NaN shows
+        const bool in = unsigned(pages[2 * r + z]) < unsigned(a.num_pages);
+        float s = best[z] * (4.f * ks[z]);
+        s = s != s ? 3.402823466e38f : fminf(fmaxf(s, -3.402823466e38f), 3.402823466e38f);
+        a.scores[(int64_t(tok) * a.hkv + h) * a.b.max_pages + p] = in ? s + 0.f : -INFINITY;
+      }
     }
-  }
   }
 }
 
 // The k largest of n scores with ties to the lower page: the k-th largest key by four 8-bit
 // radix passes, then the pages above it and the first of those equal to it, in ascending order.
 // One CTA per token and KV head. A thread keeps its KEYS keys (0: reads them again in every pass,
-// for rows of any length); scores are alike, so the lanes of a warp that meet in a bin of
-// the leading digits add up first (a bin took a thousand colliding atomics).
-constexpr int kSelectThreads = 512;
+// for rows of any length). Bound by the latency of its passes (7 us alone, 11 for 256 rows of 1000
+// pages); 512 threads, or adding up the lanes that meet in a bin first, measured 0.5 us slower.
+constexpr int kSelectThreads = 256;
 
 template <int KEYS>
 __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(SelectArgs a) {
@@ -661,13 +671,7 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(SelectArgs 
     int* hist = s_hist[pass];
     each([&](int, int p, uint32_t u) {
       const bool in = p < n && (u & fixed) == prefix;
-      const int digit = in ? int((u >> shift) & 255u) : 256;
-      if (pass < 2) {
-        const unsigned same = __match_any_sync(~0u, digit);
-        if (in && lane == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
-      } else if (in) {
-        atomicAdd(&hist[digit], 1);
-      }
+      if (in) atomicAdd(&hist[(u >> shift) & 255u], 1);
     });
     __syncthreads();
     // every warp looks for the digit of the k-th largest: lane l holds bins 255 - 8 l down to 248 - 8 l
@@ -850,14 +854,14 @@ attn_status_t attn_kv8_select(const attn_kv8_plan_t* p, const attn_kv8_cache_t* 
   a.scores = scores;
   a.selected = selected;
   const dim3 grid{unsigned(rows), unsigned(chunks)};
-  const size_t smem = size_t(a.group) * (2 * p->d + 4);
+  const size_t smem = size_t((a.group + 7) / 8 * 8) * (2 * p->d + 64 + 4);
   const attn_status_t scored = p->d == 64    ? launch(page_score_kernel<64>, grid, 128, smem, stream, a)
                                : p->d == 128 ? launch(page_score_kernel<128>, grid, 128, smem, stream, a)
                                              : launch(page_score_kernel<256>, grid, 128, smem, stream, a);
   if (scored != ATTN_OK) return scored;
   const dim3 each{unsigned(rows)};
-  if (b->max_pages_per_seq <= 2 * kSelectThreads) return launch(page_select_kernel<2>, each, kSelectThreads, 0, stream, a);
-  if (b->max_pages_per_seq <= 8 * kSelectThreads) return launch(page_select_kernel<8>, each, kSelectThreads, 0, stream, a);
+  if (b->max_pages_per_seq <= 4 * kSelectThreads) return launch(page_select_kernel<4>, each, kSelectThreads, 0, stream, a);
+  if (b->max_pages_per_seq <= 16 * kSelectThreads) return launch(page_select_kernel<16>, each, kSelectThreads, 0, stream, a);
   return launch(page_select_kernel<0>, each, kSelectThreads, 0, stream, a);
 }
 

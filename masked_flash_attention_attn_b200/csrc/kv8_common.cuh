@@ -54,14 +54,19 @@ struct Batch {
     if (cu_q == nullptr) {
       b = t;
     } else {
-      int x = 0, y = batch;       // the largest b with cu[b] <= t
-      while (y - x > 1) {
-        const int m = (x + y) >> 1;
-        if (cu(m) <= t) x = m; else y = m;
+      b = t < batch ? t : batch - 1;        // one token each is common
+      int c0 = cu(b), c1 = cu(b + 1);
+      if (c0 > t || c1 <= t) {
+        int x = 0, y = batch;     // the largest b with cu[b] <= t
+        while (y - x > 1) {
+          const int m = (x + y) >> 1;
+          if (cu(m) <= t) x = m; else y = m;
+        }
+        b = x;
+        c0 = cu(b), c1 = cu(b + 1);
       }
-      b = x;
-      i = t - cu(b);
-      nq = cu(b + 1) - cu(b);
+      i = t - c0;
+      nq = c1 - c0;
       if (i < 0 || i >= nq) return false;
     }
     n = len(b);
