@@ -75,12 +75,22 @@ struct FwdArgs {
   uint32_t* counters;
 };
 
-template <int D, int NG>
+// A CTA of W warps. Merging the warps and starting on the next item cost about as many instructions as
+// 27 steps in a CTA of 8 warps, in proportion less in one of 2; many warps leave fewer parts of few
+// long items to join. Both sides measured at d = 128, 8 KV heads, 32 query heads, 250-400 MB of codes:
+//   512 items of 2-4 K keys:    75.3 us with 8 warps, 80.5 with 2
+//   1024 items of 1-2 K keys:   80.6, 79.0
+//   8192 items of 150-300 keys: 178,  127
+// so CTAs of 2 warps from kManyItems items on (requests, or tokens with selected pages, times KV heads).
+constexpr int kManyItems = 1200;
+
+template <int D, int NG, int W>
 struct Cfg {
   static constexpr int ROWS = 8 * NG;
-  static constexpr int WARPS = NG == 1 && D <= 128 ? 8 : 4;   // 8: 128 registers and two CTAs per SM
+  static constexpr bool NARROW = NG == 1 && D <= 128;  // 128 registers: 16 warps per SM, else 8
+  static constexpr int WARPS = W;
   static constexpr int STAGES = NG >= 4 ? 4 : 3;       // >= NG: the merge overlays the ring
-  static constexpr int CTAS = 2;                       // per SM
+  static constexpr int CTAS = (NARROW ? 16 : 8) / W;   // per SM
   static constexpr int KI = D / 64;                    // 16-byte K vectors per lane and key
   static constexpr int VB = D / 8;                     // V bytes per lane and key
   static constexpr int STAGE_BYTES = 32 * D;           // 16 keys of K and of V
@@ -185,9 +195,9 @@ __device__ __forceinline__ Unit unit_of(const FwdArgs& a, int u) {
   return x;
 }
 
-template <int D, int NG>
-__global__ void __launch_bounds__(32 * Cfg<D, NG>::WARPS, Cfg<D, NG>::CTAS) kv8_fwd_kernel(FwdArgs a) {
-  using C = Cfg<D, NG>;
+template <int D, int NG, int W>
+__global__ void __launch_bounds__(32 * W, Cfg<D, NG, W>::CTAS) kv8_fwd_kernel(FwdArgs a) {
+  using C = Cfg<D, NG, W>;
   constexpr int ROWS = C::ROWS, KI = C::KI, S = C::STAGES, kWarps = C::WARPS, kThreads = 32 * kWarps;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long s_scan[kWarps], s_off;
@@ -727,20 +737,23 @@ __global__ void __launch_bounds__(32 * Cfg<D, NG>::WARPS, Cfg<D, NG>::CTAS) kv8_
 
 using Kernel = void (*)(FwdArgs);
 
+struct Choice {
+  Kernel kernel;
+  int smem, ctas, threads;
+};
+
 template <int D, int NG>
-void pick(Kernel& k, int& smem, int& ctas, int& threads) {
-  k = kv8_fwd_kernel<D, NG>;
-  smem = Cfg<D, NG>::SMEM;
-  ctas = Cfg<D, NG>::CTAS;
-  threads = 32 * Cfg<D, NG>::WARPS;
+Choice pick(bool many) {
+  constexpr int FEW = Cfg<D, NG, 2>::NARROW ? 8 : 4;
+  if (many) return {kv8_fwd_kernel<D, NG, 2>, Cfg<D, NG, 2>::SMEM, Cfg<D, NG, 2>::CTAS, 64};
+  return {kv8_fwd_kernel<D, NG, FEW>, Cfg<D, NG, FEW>::SMEM, Cfg<D, NG, FEW>::CTAS, 32 * FEW};
 }
 
 // head_dim 256: at most 16 rows (the accumulators of 32 would take every register)
-bool kernel_of(int d, int ng, Kernel& k, int& smem, int& ctas, int& threads) {
-  if (d == 64) ng == 1 ? pick<64, 1>(k, smem, ctas, threads) : ng == 2 ? pick<64, 2>(k, smem, ctas, threads) : pick<64, 4>(k, smem, ctas, threads);
-  else if (d == 128) ng == 1 ? pick<128, 1>(k, smem, ctas, threads) : ng == 2 ? pick<128, 2>(k, smem, ctas, threads) : pick<128, 4>(k, smem, ctas, threads);
-  else ng == 1 ? pick<256, 1>(k, smem, ctas, threads) : pick<256, 2>(k, smem, ctas, threads);
-  return k != nullptr;
+Choice choice_of(int d, int ng, bool many) {
+  if (d == 64) return ng == 1 ? pick<64, 1>(many) : ng == 2 ? pick<64, 2>(many) : pick<64, 4>(many);
+  if (d == 128) return ng == 1 ? pick<128, 1>(many) : ng == 2 ? pick<128, 2>(many) : pick<128, 4>(many);
+  return ng == 1 ? pick<256, 1>(many) : pick<256, 2>(many);
 }
 
 }  // namespace
@@ -776,19 +789,19 @@ attn_status_t attn_kv8_plan(const attn_kv8_problem_t* problem, attn_kv8_plan_t**
   pl->window = p.window;
   const int64_t rows = int64_t(p.hq / p.hkv) * p.max_q_len;
   pl->ng = rows <= 8 ? 1 : rows <= 16 || p.head_dim == 256 ? 2 : 4;
-  Kernel k = nullptr;
-  int smem = 0, ctas = 0, threads = 0, sms = 0;
-  kernel_of(pl->d, pl->ng, k, smem, ctas, threads);
+  int sms = 0;
   cudaError_t e = cudaGetDevice(&pl->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, pl->device);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) {
+  for (int many = 0; many < 2; ++many) {
+    const Choice c = choice_of(pl->d, pl->ng, many);
     int fit = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, k, threads, smem);
-    pl->grid = sms * std::max(1, std::min(fit, ctas));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(c.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, c.smem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, c.kernel, c.threads, c.smem);
+    pl->grid[many] = sms * std::max(1, std::min(fit, c.ctas));
   }
-  const size_t tile = size_t(8) * pl->ng, slots = size_t(2) * pl->grid;
-  const size_t bytes_o = slots * tile * pl->d * 4, bytes_ml = slots * tile * 8, bytes_c = size_t(pl->grid) * 4;
+  const int grid = std::max(pl->grid[0], pl->grid[1]);
+  const size_t tile = size_t(8) * pl->ng, slots = size_t(2) * grid;
+  const size_t bytes_o = slots * tile * pl->d * 4, bytes_ml = slots * tile * 8, bytes_c = size_t(grid) * 4;
   if (e == cudaSuccess) {
     e = cudaMalloc(&pl->ws, bytes_o + bytes_ml + bytes_c);
     if (e == cudaSuccess) {
@@ -846,10 +859,9 @@ attn_status_t attn_kv8_fwd(const attn_kv8_plan_t* p, const attn_kv8_cache_t* c, 
   a.part_o = p->part_o;
   a.part_ml = p->part_ml;
   a.counters = p->counters;
-  Kernel k = nullptr;
-  int smem = 0, ctas = 0, threads = 0;
-  kernel_of(p->d, p->ng, k, smem, ctas, threads);
-  return launch(k, dim3(p->grid), threads, smem, stream, a);
+  const int many = int64_t(selected ? b->total_q : b->batch) * p->hkv >= kManyItems;
+  const Choice k = choice_of(p->d, p->ng, many);
+  return launch(k.kernel, dim3(p->grid[many]), k.threads, k.smem, stream, a);
 }
 
 }  // extern "C"

@@ -14,12 +14,12 @@ struct attn_kv8_plan {
   float scale = 0.f;
   int32_t mask = 0, window = 0;
   int32_t ng = 1;                 // row tile of the attention kernel: 8 ng rows
-  int32_t grid = 0;               // persistent CTAs
+  int32_t grid[2] = {0, 0};       // persistent CTAs: of few and of many items
   int32_t device = 0;
   void* ws = nullptr;             // partial results and counters
-  float* part_o = nullptr;        // [2 grid][8 ng][d]
-  float* part_ml = nullptr;       // [2 grid][8 ng][2]
-  uint32_t* counters = nullptr;   // [grid], zero between launches
+  float* part_o = nullptr;        // [2 CTAs][8 ng][d]
+  float* part_ml = nullptr;       // [2 CTAs][8 ng][2]
+  uint32_t* counters = nullptr;   // [CTAs], zero between launches
 };
 
 namespace kv8 {

@@ -268,10 +268,13 @@ def test_long_contexts_are_split_over_ctas(d, hq, hkv):
     attend(22, [9000], [3], hq=hq, hkv=hkv, d=d, page=16, sample=12)
 
 
-def test_many_short_requests():
+@pytest.mark.parametrize("d,hq,hkv,q", [(64, 8, 4, 1), (128, 8, 4, 1), (256, 4, 4, 1), (64, 8, 4, 6), (128, 32, 4, 2), (128, 32, 4, 4),
+                                        (256, 16, 4, 3)])
+def test_many_short_requests(d, hq, hkv, q):
     rng = np.random.default_rng(3)
-    lens = list(rng.integers(1, 90, 700))
-    attend(30, lens, [1] * 700, hq=8, hkv=4, d=64, page=16, sample=500)
+    lens = [int(x) for x in rng.integers(q, 90, 350)]
+    lens[7], lens[200] = 2000, 1500
+    attend(30, lens, [q] * 350, hq=hq, hkv=hkv, d=d, page=16, sample=300)
 
 
 @pytest.mark.parametrize("d,hq,hkv,page", [(128, 8, 2, 64), (64, 2, 2, 16), (256, 4, 2, 32)])
