@@ -242,11 +242,12 @@ __global__ void __launch_bounds__(32 * W, Cfg<D, NG, W>::CTAS) kv8_fwd_kernel(Fw
     int sum[kTries] = {};                         // pieces at each length
     for (int u = u0; u < u1; ++u) {
       const Unit x = my_unit(u);
-      const unsigned items = x.tiles * a.hkv;
+      // in floating point: an estimate one off only moves a piece to a CTA that has one
+      const float items = float(x.tiles) * float(a.hkv);
 #pragma unroll
       for (int j = 0; j < kTries; ++j) {
-        const unsigned len = mean + 1 + unsigned(mean) * j / 16;
-        sum[j] += int(min((unsigned long long)items * ((unsigned(x.chunks) + len - 1) / len), 0x100000ull));
+        const float len = float(mean + 1 + mean * j / 16);
+        sum[j] += int(fminf(items * ceilf(__fdividef(float(x.chunks), len)), 1e6f));
       }
     }
 #pragma unroll
@@ -255,12 +256,14 @@ __global__ void __launch_bounds__(32 * W, Cfg<D, NG, W>::CTAS) kv8_fwd_kernel(Fw
       if (lane == 0) s_sum[j][warp] = sum[j];
     }
     __syncthreads();
-    for (int j = kTries - 1; j >= 0; --j) {
-      int pieces = 0;
-      for (int w = 0; w < kWarps; ++w) pieces += s_sum[j][w];
-      const int len = mean + 1 + mean * j / 16;
-      if (pieces <= int(gridDim.x) && len <= mean + kPiece) T = len;
-    }
+    // lane j looks at length j
+    int pieces = 0;
+    if (lane < kTries)
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) pieces += s_sum[lane][w];
+    const int len = mean + 1 + mean * lane / 16;
+    const unsigned fits = __ballot_sync(~0u, lane < kTries && pieces <= int(gridDim.x) && len <= mean + kPiece);
+    if (fits) T = __shfl_sync(~0u, len, __ffs(fits) - 1);
     if (T == 0) break;
   }
   const int G = int(min((long long)gridDim.x, total));
@@ -712,7 +715,7 @@ __global__ void __launch_bounds__(32 * W, Cfg<D, NG, W>::CTAS) kv8_fwd_kernel(Fw
             Z[k] = fmaf(Z[k], e0, zs);
             acc[k].x *= e0, acc[k].y *= e0, acc[k].z *= e0, acc[k].w *= e0;
           }
-#pragma unroll 4
+#pragma unroll(N == 1 ? 8 : 4)
           for (int c = 0; c < nb; ++c) {
             const int slot = b0 + c == 0 ? odd : 2 * (b0 + c);
 #pragma unroll
