@@ -782,7 +782,7 @@ attn_status_t attn_kv8_append(const attn_kv8_cache_t* c, const void* k_new, int6
   a.shift = shift_of(c->page_size);
   a.num_slots = c->num_pages * c->page_size;
   // tokens per CTA: enough that the grid is about one wave of 148 x 16 CTAs, at most half a page (a CTA then has
-  // one run or none: 17.5 us for 13.7 K tokens of 8 x 128 against 18.3 with whole pages, floor 10.2)
+  // one run or none: 17.5 us for 10.8 K tokens of 8 x 128 against 18.3 with whole pages, floor 10.2)
   int span = 1;
   while (2 * span < c->page_size && int64_t(num_tokens) * c->hkv * 2 >= int64_t(2 * span) * 148 * 16) span *= 2;
   a.span = span;
