@@ -214,7 +214,7 @@ __device__ __noinline__ uint32_t without_nan(uint32_t w, unsigned& top) {
 
 template <int NT, int NV>
 __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 8) append_kernel(AppendArgs a) {
-  constexpr int kEnd = -2;        // slot of the tokens before the first and behind the last
+  constexpr int kEnd = -2;        // slot of the tokens before the first and behind the last; -1: a skipped token
   __shared__ int s_slot[260];     // of the tokens t0 - 1 .. t0 + span + page_size - 1
   __shared__ int s_list[128];
   __shared__ int s_count, s_stop, s_taken[NT / 32];
@@ -232,7 +232,8 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 8) append_kernel(AppendArg
   wait_for_previous_kernel();
   for (int j = tid; j <= a.span + ps; j += NT) {
     const int t = t0 - 1 + j;
-    s_slot[j] = t >= 0 && t < a.tokens ? a.slots[t] : kEnd;
+    const int s = t >= 0 && t < a.tokens ? a.slots[t] : kEnd;
+    s_slot[j] = valid(s) ? s : t >= 0 && t < a.tokens ? -1 : kEnd;
   }
   __syncthreads();
   if (tid < a.span && valid(s_slot[tid + 1])) {

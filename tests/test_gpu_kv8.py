@@ -154,9 +154,10 @@ def test_append_strided_views_and_skipped_slots():
     assert not k.is_contiguous()
     cache = H.make_cache(5, 8, hkv, page, d, -14, -9)
     slots = slots_for(H.make_table(6, [64], page, 8), [7], [50], page)
-    slots[10:13] = -1
+    slots[10:13] = [-1, -2, -3]
     slots[30] = 8 * page                         # past the cache
     slots[31] = -2 ** 31
+    slots[40] = -2
     check_append(cache, k, v, slots, page)
 
 
