@@ -208,6 +208,7 @@ __global__ void __launch_bounds__(32 * W, Cfg<D, NG, W>::CTAS) kv8_fwd_kernel(Fw
   const int ps = 1 << a.b.page_shift;
 
   wait_for_previous_kernel();
+  if (tid == 0) s_unit = 0, s_off = 0;
   // ---- this CTA's part [line0, line1) of the line of places (T > 0: pieces, else chunks and starts) ----
   const int units = a.selected ? a.b.total_q : a.b.batch;
   const int per = (units + kThreads - 1) / kThreads, u0 = min(units, tid * per), u1 = min(units, u0 + per);
@@ -311,8 +312,8 @@ __global__ void __launch_bounds__(32 * W, Cfg<D, NG, W>::CTAS) kv8_fwd_kernel(Fw
   for (long long line = line0; line < line1;) {
     const Unit x = unit_of<ROWS, kWarps>(a, unit);
     const long long unit_chunks = line_of(x);
-    if (off >= unit_chunks) {                     // a unit without tokens
-      ++unit;
+    if (off >= unit_chunks) {                     // a unit without tokens, or done with
+      if (++unit >= units) break;                 // (only if the lengths change while the kernel runs)
       off = 0;
       continue;
     }
