@@ -27,9 +27,9 @@ first: type, shape, layout, device (all on one CUDA device, which must be the cu
 from __future__ import annotations
 
 import ctypes
-from typing import Optional
+import struct
 
-from . import MASK_KIND, _check, _stream, lib
+from . import MASK_KIND, _check, lib
 
 PAGE_SIZES = (16, 32, 64, 128)
 
@@ -60,13 +60,20 @@ class attn_kv8_batch_t(ctypes.Structure):
                 ("max_pages_per_seq", ctypes.c_int32), ("kv_lens", ctypes.c_void_p)]
 
 
+# attn_page_tables_t and attn_kv8_batch_t as a call fills them (a ctypes structure takes three times as long)
+_TABLES = struct.Struct("5i10P").pack
+_BATCH = struct.Struct("Pq2i2PiP").pack
+
 torch = None                       # imported with the first cache, plan or call, as elsewhere in this package
-_I32 = _F32 = _BF16 = _E4M3 = _I8 = None
+_I32 = _F32 = _BF16 = _E4M3 = _I8 = _device = _raw_stream = None
 
 
 def _init():
-    global torch, _I32, _F32, _BF16, _E4M3, _I8
+    global torch, _I32, _F32, _BF16, _E4M3, _I8, _device, _raw_stream
     import torch as t
+    # without the initialisation checks of torch.cuda's: they are asked when there is a tensor on a CUDA device
+    _device = getattr(t._C, "_cuda_getDevice", None) or t.cuda.current_device
+    _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or (lambda dev: t.cuda.current_stream(dev).cuda_stream)
     _I32, _F32, _BF16, _E4M3, _I8 = t.int32, t.float32, t.bfloat16, t.float8_e4m3fn, t.int8
     torch = t
 
@@ -94,21 +101,37 @@ def _ptr(t, name, dtype, shape, dev):
     _wrong(t, name, dtype, shape, dev)
 
 
-def _shape(t, name, dims):
-    """The shape of a tensor of ``dims`` dimensions."""
+def _i32s(tensors, names, shapes, dev):
+    """_ptr() of several int32 tensors."""
+    at = []
     try:
-        if len(t.shape) == dims:
-            return t.shape
+        for t, shape in zip(tensors, shapes):
+            if not (t.dtype is _I32 and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
+                break
+            at.append(t.data_ptr())
+        else:
+            return at
     except AttributeError:
         pass
+    _wrong(tensors[len(at)], names[len(at)], _I32, shapes[len(at)], dev)
+
+
+def _shape(t, name, dims):
+    """The shape of a tensor of ``dims`` dimensions."""
+    if isinstance(t, torch.Tensor) and len(t.shape) == dims:
+        return t.shape
     _wrong(t, name, getattr(t, "dtype", None), (None,) * dims, -1)
 
 
 def _rows(t, name, heads, head_dim, dev):
     """(pointer, elements from token to token, tokens) of bf16 rows [tokens][heads][head_dim]; the rows may lie
     apart (a view of a fused projection), each row is contiguous."""
-    n = _shape(t, name, 3)[0]
-    if t.dtype is not _BF16 or t.shape != (n, heads, head_dim) or t.get_device() != dev:
+    try:
+        n, th, td = t.shape
+        right = t.dtype is _BF16 and th == heads and td == head_dim and t.get_device() == dev
+    except (AttributeError, ValueError):          # not a tensor, or not of three dimensions
+        right = False
+    if not right:
         _wrong(t, name, _BF16, (None, heads, head_dim), dev)
     row = heads * head_dim
     if t.is_contiguous():
@@ -126,13 +149,14 @@ def _on_current(dev, stream):
     """The raw stream of a call whose tensors are on device ``dev``."""
     if dev < 0:
         raise ValueError("the tensors must be CUDA tensors")
-    if torch.cuda.current_device() != dev:
-        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
-    if stream is not None:
-        at = getattr(stream, "device", None)
-        if at is not None and at.index != dev:
-            raise ValueError(f"the stream is on {at}, the tensors on cuda:{dev}")
-    return _stream(stream)
+    if _device() != dev:
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{_device()}")
+    if stream is None:
+        return _raw_stream(dev)
+    at = getattr(stream, "device", None)
+    if at is not None and at.index != dev:
+        raise ValueError(f"the stream is on {at}, the tensors on cuda:{dev}")
+    return getattr(stream, "cuda_stream", stream)
 
 
 class Kv8Cache:
@@ -205,19 +229,22 @@ def attn_page_tables(*, page_table, old_lens, new_lens, free_pages, free_state, 
     [batch + 1], slots and positions [max_tokens] are written."""
     if torch is None:
         _init()
-    batch, = _shape(old_lens, "old_lens", 1)
-    tokens, = _shape(slots, "slots", 1)
-    pages, = _shape(free_pages, "free_pages", 1)
-    width = _shape(page_table, "page_table", 2)[1]
-    dev, lens = old_lens.get_device(), (batch,)
-    a = attn_page_tables_t(
-        batch, width, pages, page_size, tokens, _ptr(page_table, "page_table", _I32, (batch, width), dev),
-        _ptr(old_lens, "old_lens", _I32, lens, dev), _ptr(new_lens, "new_lens", _I32, lens, dev),
-        _ptr(free_pages, "free_pages", _I32, (pages,), dev), _ptr(free_state, "free_state", _I32, (4,), dev),
-        _ptr(next_state, "next_state", _I32, (4,), dev), _ptr(kv_lens, "kv_lens", _I32, lens, dev),
-        _ptr(cu_seqlens_q, "cu_seqlens_q", _I32, (batch + 1,), dev), _ptr(slots, "slots", _I32, (tokens,), dev),
-        None if positions is None else _ptr(positions, "positions", _I32, (tokens,), dev))
-    st = lib().attn_page_tables(ctypes.byref(a), _on_current(dev, stream))
+    try:
+        (batch,), (tokens,), (pages,), (_, width) = old_lens.shape, slots.shape, free_pages.shape, page_table.shape
+        dev = old_lens.get_device()
+    except (AttributeError, ValueError):
+        for t, name, dims in ((old_lens, "old_lens", 1), (slots, "slots", 1), (free_pages, "free_pages", 1), (page_table, "page_table", 2)):
+            _shape(t, name, dims)
+        raise
+    lens, four = (batch,), (4,)
+    at = _i32s((page_table, old_lens, new_lens, free_pages, free_state, next_state, kv_lens, cu_seqlens_q, slots,
+                slots if positions is None else positions),
+               ("page_table", "old_lens", "new_lens", "free_pages", "free_state", "next_state", "kv_lens", "cu_seqlens_q", "slots", "positions"),
+               ((batch, width), lens, lens, (pages,), four, four, lens, (batch + 1,), (tokens,), (tokens,)), dev)
+    if positions is None:
+        at[9] = 0
+    a = _TABLES(batch, width, pages, page_size, tokens, *at)
+    st = lib().attn_page_tables(a, _on_current(dev, stream))
     if st:
         _check(st, "attn_page_tables")
 
@@ -288,17 +315,22 @@ def _batch(plan, cache, q, page_table, kv_lens, cu_seqlens_q):
     if dev != plan.index:
         raise ValueError(f"the cache is on {cache.device}, the plan on cuda:{plan.index}")
     qp, stride, total = _rows(q, "q", plan.hq, plan.head_dim, dev)
-    batch, = _shape(kv_lens, "kv_lens", 1)
-    rows, width = _shape(page_table, "page_table", 2)
+    try:
+        (batch,), (rows, width) = kv_lens.shape, page_table.shape
+    except (AttributeError, ValueError):
+        _shape(kv_lens, "kv_lens", 1), _shape(page_table, "page_table", 2)
+        raise
     if rows < batch:
         raise ValueError(f"page_table has {rows} rows for {batch} requests")
-    cp = None
     if cu_seqlens_q is not None:
-        cp = _ptr(cu_seqlens_q, "cu_seqlens_q", _I32, (batch + 1,), dev)
-    elif total != batch:
-        raise ValueError(f"q has {total} tokens for {batch} requests: cu_seqlens_q is required")
-    return attn_kv8_batch_t(qp, stride, batch, total, cp, _ptr(page_table, "page_table", _I32, (rows, width), dev), width,
-                            _ptr(kv_lens, "kv_lens", _I32, (batch,), dev)), total, width, dev
+        tp, lp, cp = _i32s((page_table, kv_lens, cu_seqlens_q), ("page_table", "kv_lens", "cu_seqlens_q"),
+                           ((rows, width), (batch,), (batch + 1,)), dev)
+    else:
+        if total != batch:
+            raise ValueError(f"q has {total} tokens for {batch} requests: cu_seqlens_q is required")
+        tp, lp = _i32s((page_table, kv_lens), ("page_table", "kv_lens"), ((rows, width), (batch,)), dev)
+        cp = 0
+    return _BATCH(qp, stride, batch, total, cp, tp, width, lp), total, width, dev
 
 
 def attn_kv8_fwd(plan: Kv8Plan, cache: Kv8Cache, q, page_table, kv_lens, out, lse=None, *, cu_seqlens_q=None,
@@ -316,7 +348,7 @@ def attn_kv8_fwd(plan: Kv8Plan, cache: Kv8Cache, q, page_table, kv_lens, out, ls
         if n < 1:
             raise ValueError("selected must list at least one page")
         sp = _ptr(selected, "selected", _I32, (total, plan.hkv, n), dev) or None   # no tokens
-    st = lib().attn_kv8_fwd(plan.handle, cache._ref, ctypes.byref(b), sp, n, op, lp, _on_current(dev, stream))
+    st = lib().attn_kv8_fwd(plan.handle, cache._ref, b, sp, n, op, lp, _on_current(dev, stream))
     if st:
         _check(st, "attn_kv8_fwd")
 
@@ -332,7 +364,7 @@ def attn_kv8_select(plan: Kv8Plan, cache: Kv8Cache, q, page_table, kv_lens, scor
     n = _shape(selected, "selected", 3)[2]
     cp = _ptr(scores, "scores", _F32, (total, plan.hkv, width), dev)
     sp = _ptr(selected, "selected", _I32, (total, plan.hkv, n), dev)
-    st = lib().attn_kv8_select(plan.handle, cache._ref, ctypes.byref(b), int(sink), int(recent), cp, sp, n,
+    st = lib().attn_kv8_select(plan.handle, cache._ref, b, int(sink), int(recent), cp, sp, n,
                                _on_current(dev, stream))
     if st:
         _check(st, "attn_kv8_select")
