@@ -519,14 +519,100 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The queries of a token and head h in int8: s_q [heads in eights][2 D], s_unit as many units (-inf: no head)
+template <int D>
+struct Queries {
+  static constexpr int PITCH = 2 * D / 16 + 4;   // vectors; neighbouring heads half a line apart: no bank conflicts
+  uint4* s_q;
+  float* s_unit;
+  int eights;
+  __device__ __forceinline__ Queries(const SelectArgs& a, uint4* smem) {
+    eights = (a.group + 7) >> 3;
+    s_q = smem;
+    s_unit = reinterpret_cast<float*>(smem + eights * 8 * PITCH);
+  }
+  __device__ __forceinline__ void quantise(const SelectArgs& a, int tok, int h, int warps) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    for (int r = threadIdx.x >> 5; r < 8 * eights; r += warps) {
+      int8_t* dst = reinterpret_cast<int8_t*>(s_q + r * PITCH) + lane * E;
+      const bool live = r < a.group;
+      const __nv_bfloat16* q = a.q + int64_t(tok) * a.q_stride + int64_t(h * a.group + (live ? r : 0)) * D + lane * E;
+      float f[E];
+      unsigned top = 0;
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        f[j] = live ? __bfloat162float(q[j]) : 0.f;
+        const unsigned m = (__float_as_uint(f[j]) >> 16) & 0x7fffu;
+        if (m < 0x7f80u) top = max(top, m);
+      }
+      top = __reduce_max_sync(~0u, top);
+      // 127 = 1.984375 * 2^6: significand 126 / 128 over 1
+      const int e = max(-126, int(top >> 7) - 127 - 6 + ((top & 127u) > 126u ? 1 : 0));
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const int qi = min(127, max(-127, __float2int_rn(f[j] * __int_as_float((127 - e) << 23))));   // NaN converts to 0
+        dst[j] = int8_t(max(qi, 0));
+        dst[D + j] = int8_t(min(qi, 0));
+      }
+      if (lane == 0) s_unit[r] = live ? __int_as_float((e + 127) << 23) : -INFINITY;
+    }
+  }
+};
+
+// Bounds of the pages pg[0], pg[1] that lane (g, t) has (g = 0 .. 7: sixteen pages a warp), and their scores
+template <int D>
+struct PagePair {
+  static constexpr int VEC = D / 32;             // 16-byte vectors per lane and page
+  uint4 w[2][VEC];
+  float ks[2];
+  __device__ __forceinline__ void load(const SelectArgs& a, int h, const int* pg, int t) {
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const bool in = unsigned(pg[z]) < unsigned(a.num_pages);
+      const int64_t block = in ? int64_t(pg[z]) * a.hkv + h : 0;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        w[z][i] = in ? __ldg(reinterpret_cast<const uint4*>(a.bounds + block * (2 * D)) + 4 * i + t) : make_uint4(0, 0, 0, 0);
+      ks[z] = in ? __ldg(a.k_scale + block) : 0.f;
+    }
+  }
+  __device__ __forceinline__ void score(const SelectArgs& a, const Queries<D>& q, const int* pg, int g, int t, float (&s)[2]) const {
+    float best[2] = {-INFINITY, -INFINITY};
+    for (int e = 0; e < q.eights; ++e) {
+      int dot[4] = {0, 0, 0, 0};  // pages g, g, g + 8, g + 8 and heads 2t, 2t + 1, 2t, 2t + 1
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const uint4 c = q.s_q[(8 * e + g) * Queries<D>::PITCH + 4 * i + t];
+        mma_s8(dot, w[0][i].x, w[1][i].x, w[0][i].y, w[1][i].y, c.x, c.y);
+        mma_s8(dot, w[0][i].z, w[1][i].z, w[0][i].w, w[1][i].w, c.z, c.w);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float unit = q.s_unit[8 * e + 2 * t + j];
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+          best[z] = fmaxf(best[z], unit > 0.f ? float(dot[2 * z + j]) * unit : -INFINITY);
+      }
+    }
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      best[z] = fmaxf(best[z], __shfl_xor_sync(~0u, best[z], 1));
+      best[z] = fmaxf(best[z], __shfl_xor_sync(~0u, best[z], 2));
+      // finite, so that the pages that are always selected stay above it; a page that holds a NaN
+      // comes first of the others, so that the NaN shows
+      float x = best[z] * (4.f * ks[z]);
+      x = x != x ? 3.402823466e38f : fminf(fmaxf(x, -3.402823466e38f), 3.402823466e38f);
+      s[z] = unsigned(pg[z]) < unsigned(a.num_pages) ? x + 0.f : -INFINITY;
+    }
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(128) page_score_kernel(SelectArgs a) {
-  extern __shared__ uint4 s_q[];  // [heads in eights][2 D] int8, then as many units (-inf: no head)
-  constexpr int VEC = D / 32;     // 16-byte vectors per lane and page
+  extern __shared__ uint4 s_q[];
   constexpr int ROUNDS = kScorePages / 64;
-  constexpr int PITCH = 2 * D / 16 + 4;   // vectors; neighbouring heads half a line apart: no bank conflicts
-  const int eights = (a.group + 7) >> 3;
-  float* s_unit = reinterpret_cast<float*>(s_q + eights * 8 * PITCH);
+  Queries<D> queries(a, s_q);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int tok = blockIdx.x / a.hkv, h = blockIdx.x - tok * a.hkv;
   const int p0 = blockIdx.y * kScorePages;
@@ -543,111 +629,42 @@ __global__ void __launch_bounds__(128) page_score_kernel(SelectArgs a) {
     const int p = first + 64 * (r >> 1) + 8 * (r & 1);
     pages[r] = p < n ? __ldg(a.b.page_table + int64_t(b) * a.b.max_pages + p) : -1;
   }
-
-  for (int r = warp; r < 8 * eights; r += 4) {
-    constexpr int E = D / 32;
-    int8_t* dst = reinterpret_cast<int8_t*>(s_q + r * PITCH) + lane * E;
-    const bool live = r < a.group;
-    const __nv_bfloat16* q = a.q + int64_t(tok) * a.q_stride + int64_t(h * a.group + (live ? r : 0)) * D + lane * E;
-    float f[E];
-    unsigned top = 0;
-#pragma unroll
-    for (int j = 0; j < E; ++j) {
-      f[j] = live ? __bfloat162float(q[j]) : 0.f;
-      const unsigned m = (__float_as_uint(f[j]) >> 16) & 0x7fffu;
-      if (m < 0x7f80u) top = max(top, m);
-    }
-    top = __reduce_max_sync(~0u, top);
-    // 127 = 1.984375 * 2^6: significand 126 / 128 over 1
-    const int e = max(-126, int(top >> 7) - 127 - 6 + ((top & 127u) > 126u ? 1 : 0));
-#pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const int qi = min(127, max(-127, __float2int_rn(f[j] * __int_as_float((127 - e) << 23))));   // NaN converts to 0
-      dst[j] = int8_t(max(qi, 0));
-      dst[D + j] = int8_t(min(qi, 0));
-    }
-    if (lane == 0) s_unit[r] = live ? __int_as_float((e + 127) << 23) : -INFINITY;
-  }
+  queries.quantise(a, tok, h, 4);
   __syncthreads();
-
 #pragma unroll
   for (int r = 0; r < ROUNDS; ++r) {
-    uint4 w[2][VEC];
-    float ks[2], best[2] = {-INFINITY, -INFINITY};
+    PagePair<D> x;
+    x.load(a, h, pages + 2 * r, t);
+    float s[2];
+    x.score(a, queries, pages + 2 * r, g, t, s);
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
-      const bool in = unsigned(pages[2 * r + z]) < unsigned(a.num_pages);
-      const int64_t block = in ? int64_t(pages[2 * r + z]) * a.hkv + h : 0;
-#pragma unroll
-      for (int i = 0; i < VEC; ++i)
-        w[z][i] = in ? __ldg(reinterpret_cast<const uint4*>(a.bounds + block * (2 * D)) + 4 * i + t) : make_uint4(0, 0, 0, 0);
-      ks[z] = in ? __ldg(a.k_scale + block) : 0.f;
-    }
-    for (int e = 0; e < eights; ++e) {
-      int dot[4] = {0, 0, 0, 0};  // pages g, g, g + 8, g + 8 and heads 2t, 2t + 1, 2t, 2t + 1
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const uint4 c = s_q[(8 * e + g) * PITCH + 4 * i + t];
-        mma_s8(dot, w[0][i].x, w[1][i].x, w[0][i].y, w[1][i].y, c.x, c.y);
-        mma_s8(dot, w[0][i].z, w[1][i].z, w[0][i].w, w[1][i].w, c.z, c.w);
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float unit = s_unit[8 * e + 2 * t + j];
-#pragma unroll
-        for (int z = 0; z < 2; ++z)
-          best[z] = fmaxf(best[z], unit > 0.f ? float(dot[2 * z + j]) * unit : -INFINITY);
-      }
-    }
-#pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      best[z] = fmaxf(best[z], __shfl_xor_sync(~0u, best[z], 1));
-      best[z] = fmaxf(best[z], __shfl_xor_sync(~0u, best[z], 2));
       const int p = first + 64 * r + 8 * z;
-      if (t == 0 && p < n) {
-        // finite, so that the pages that are always selected stay above it; a page that holds a NaN
-        // comes first of the others, so that the NaN shows
-        const bool in = unsigned(pages[2 * r + z]) < unsigned(a.num_pages);
-        float s = best[z] * (4.f * ks[z]);
-        s = s != s ? 3.402823466e38f : fminf(fmaxf(s, -3.402823466e38f), 3.402823466e38f);
-        a.scores[(int64_t(tok) * a.hkv + h) * a.b.max_pages + p] = in ? s + 0.f : -INFINITY;
-      }
+      if (t == 0 && p < n) a.scores[(int64_t(tok) * a.hkv + h) * a.b.max_pages + p] = s[z];
     }
   }
 }
 
 // The k largest of n scores with ties to the lower page: the k-th largest key by four 8-bit
-// radix passes, then the pages above it and the first of those equal to it, in ascending order.
+// radix passes at most (a pass ends the search when the k-th largest is the last of its bin), then the
+// pages above it and the first of those equal to it, in ascending order.
 // One CTA per token and KV head. A thread keeps its KEYS keys (0: reads them again in every pass,
-// for rows of any length). Bound by the latency of its passes (7 us alone, 11 for 256 rows of 1000
-// pages); 512 threads, or adding up the lanes that meet in a bin first, measured 0.5 us slower.
+// for rows of any length). Bound by the latency of its passes; 512 threads, or adding up the lanes
+// that meet in a bin first, measured 0.5 us slower.
 constexpr int kSelectThreads = 256;
+// Scores and selection are one launch, by one CTA a row, where that CTA's part is short or there are rows for
+// all SMs; else the scores are spread over more CTAs. Measured (8 rows to a token, d = 128; one launch, two):
+//   tokens x pages   1 x 64: 3.8 us, 5.6   1 x 512: 6.8, 7.0   1 x 1000: 10.0, 7.8   8 x 1000: 10.2, 9.4
+//                    16 x 1000: 10.8, 12.2   32 x 1000: 18.5, 21.7   1024 x 128: 92, 112
+constexpr int kFuse = 512;                // pages of a table row that one launch takes with any number of rows,
+constexpr int kFuseRows = 96;             // rows from which on it takes 4 kSelectThreads
 
-template <int KEYS>
-__global__ void __launch_bounds__(kSelectThreads) page_select_kernel(SelectArgs a) {
+// the CTA's share: the pages of one token and head into `out`; load(p) is the key of page p
+template <int KEYS, class Load>
+__device__ __forceinline__ void pick_pages(int n, int k, int32_t* out, int (&s_hist)[4][256], Load load) {
   constexpr int W = kSelectThreads / 32;
-  __shared__ int s_hist[4][256];
   __shared__ int s_eq[2][W], s_gt[2][W];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < 4 * 256; i += kSelectThreads) s_hist[0][i] = 0;
-  wait_for_previous_kernel();
-  const int tok = blockIdx.x / a.hkv, h = blockIdx.x - tok * a.hkv;
-  int b, pos, len;
-  if (!a.b.token_by_warp(tok, b, pos, len)) return;
-  const int n = (a.b.hi(pos, len) + (1 << a.b.page_shift) - 1) >> a.b.page_shift;
-  const float* scores = a.scores + (int64_t(tok) * a.hkv + h) * a.b.max_pages;
-  int32_t* out = a.selected + (int64_t(tok) * a.hkv + h) * a.k;
-  for (int i = tid; i < a.k; i += kSelectThreads)
-    if (i >= n) out[i] = -1;
-  if (n <= a.k) {
-    for (int i = tid; i < n; i += kSelectThreads) out[i] = i;
-    return;
-  }
-  auto load = [&](int p) -> uint32_t {            // larger scores have larger keys
-    if (p < a.sink || p >= n - a.recent) return 0xffffffffu;
-    const uint32_t u = __float_as_uint(scores[p]);
-    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
-  };
   uint32_t keys[KEYS ? KEYS : 1];
   if constexpr (KEYS > 0) {
 #pragma unroll
@@ -665,7 +682,7 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(SelectArgs 
     }
   };
   uint32_t prefix = 0, fixed = 0;
-  int rem = a.k;                  // how many of the keys that match the prefix are taken
+  int rem = k;                    // how many of the keys that match the prefix are taken
   __syncthreads();
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass;
@@ -676,7 +693,7 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(SelectArgs 
     });
     __syncthreads();
     // every warp looks for the digit of the k-th largest: lane l holds bins 255 - 8 l down to 248 - 8 l
-    int c[8], sum = 0, digit = 0, over = 0;
+    int c[8], sum = 0, digit = 0, over = 0, count = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum += c[j] = hist[255 - 8 * lane - j];
     int inc = sum;
@@ -688,7 +705,7 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(SelectArgs 
     const bool mine = above < rem && inc >= rem;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      if (above < rem && above + c[j] >= rem) digit = 255 - 8 * lane - j, over = above;
+      if (above < rem && above + c[j] >= rem) digit = 255 - 8 * lane - j, over = above, count = c[j];
       above += c[j];
     }
     const int who = __ffs(__ballot_sync(~0u, mine)) - 1;
@@ -696,11 +713,12 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(SelectArgs 
     rem -= __shfl_sync(~0u, over, who);
     prefix |= uint32_t(digit) << shift;
     fixed |= 255u << shift;
+    if (__shfl_sync(~0u, count, who) == rem) break;   // every key that matches is taken
   }
   int eq0 = 0, gt0 = 0;           // counts before this round's pages
   each([&](int i, int p, uint32_t u) {
     if (i * kSelectThreads >= n) return;
-    const bool gt = p < n && u > prefix, eq = p < n && u == prefix;
+    const bool gt = p < n && (u & fixed) > prefix, eq = p < n && (u & fixed) == prefix;
     const unsigned mg = __ballot_sync(~0u, gt), me = __ballot_sync(~0u, eq);
     if (lane == 0) s_gt[i & 1][warp] = __popc(mg), s_eq[i & 1][warp] = __popc(me);
     __syncthreads();
@@ -716,6 +734,74 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(SelectArgs 
     e += __popc(me & below);
     if (gt || (eq && e < rem)) out[g + min(e, rem)] = p;
   });
+}
+
+// larger scores have larger keys; the pages that are always selected have the largest
+__device__ __forceinline__ uint32_t key_of(const SelectArgs& a, int n, int p, float score) {
+  if (p < a.sink || p >= n - a.recent) return 0xffffffffu;
+  const uint32_t u = __float_as_uint(score);
+  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+
+// all of n <= k pages, and the rest of the list; true if that was all
+__device__ __forceinline__ bool few_pages(const SelectArgs& a, int n, int32_t* out) {
+  for (int i = threadIdx.x; i < a.k; i += kSelectThreads)
+    if (i >= n || n <= a.k) out[i] = i < n ? i : -1;
+  return n <= a.k;
+}
+
+template <int KEYS>
+__global__ void __launch_bounds__(kSelectThreads) page_select_kernel(SelectArgs a) {
+  __shared__ int s_hist[4][256];
+  for (int i = threadIdx.x; i < 4 * 256; i += kSelectThreads) s_hist[0][i] = 0;
+  wait_for_previous_kernel();
+  const int tok = blockIdx.x / a.hkv, h = blockIdx.x - tok * a.hkv;
+  int b, pos, len;
+  if (!a.b.token_by_warp(tok, b, pos, len)) return;
+  const int n = (a.b.hi(pos, len) + (1 << a.b.page_shift) - 1) >> a.b.page_shift;
+  const float* scores = a.scores + (int64_t(tok) * a.hkv + h) * a.b.max_pages;
+  int32_t* out = a.selected + (int64_t(tok) * a.hkv + h) * a.k;
+  if (few_pages(a, n, out)) return;
+  pick_pages<KEYS>(n, a.k, out, s_hist, [&](int p) { return key_of(a, n, p, scores[p]); });
+}
+
+// Both steps in one launch, for rows of at most 256 KEYS pages
+template <int D, int KEYS>
+__global__ void __launch_bounds__(kSelectThreads, D == 256 ? 2 : 4) page_score_select_kernel(SelectArgs a) {
+  constexpr int W = kSelectThreads / 32;
+  extern __shared__ uint4 s_q[];
+  __shared__ int s_hist[4][256];
+  __shared__ float s_score[KEYS * kSelectThreads];
+  Queries<D> queries(a, s_q);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  for (int i = tid; i < 4 * 256; i += kSelectThreads) s_hist[0][i] = 0;
+  const int tok = blockIdx.x / a.hkv, h = blockIdx.x - tok * a.hkv;
+  wait_for_previous_kernel();
+  int b, pos, len;
+  if (!a.b.token_by_warp(tok, b, pos, len)) return;
+  const int n = (a.b.hi(pos, len) + (1 << a.b.page_shift) - 1) >> a.b.page_shift;
+  const int32_t* table = a.b.page_table + int64_t(b) * a.b.max_pages;
+  float* scores = a.scores + (int64_t(tok) * a.hkv + h) * a.b.max_pages;
+  int32_t* out = a.selected + (int64_t(tok) * a.hkv + h) * a.k;
+  auto look_up = [&](int p) { return p < n ? __ldg(table + p) : -1; };
+  // the lane's pages of a round: p and p + 8. The next round's are looked up while this one's bounds come
+  int p = 16 * warp + g, next[2] = {look_up(p), look_up(p + 8)};
+  queries.quantise(a, tok, h, W);
+  __syncthreads();
+  for (; p - g < n; p += 16 * W) {
+    const int now[2] = {next[0], next[1]};
+    PagePair<D> x;
+    x.load(a, h, now, t);
+    next[0] = look_up(p + 16 * W), next[1] = look_up(p + 16 * W + 8);
+    float s[2];
+    x.score(a, queries, now, g, t, s);
+#pragma unroll
+    for (int z = 0; z < 2; ++z)
+      if (t == 0 && p + 8 * z < n) scores[p + 8 * z] = s_score[p + 8 * z] = s[z];
+  }
+  if (few_pages(a, n, out)) return;
+  __syncthreads();
+  pick_pages<KEYS>(n, a.k, out, s_hist, [&](int p) { return key_of(a, n, p, s_score[p]); });
 }
 
 }  // namespace
@@ -854,15 +940,20 @@ attn_status_t attn_kv8_select(const attn_kv8_plan_t* p, const attn_kv8_cache_t* 
   a.k = n_selected;
   a.scores = scores;
   a.selected = selected;
-  const dim3 grid{unsigned(rows), unsigned(chunks)};
+  const dim3 grid{unsigned(rows), unsigned(chunks)}, each{unsigned(rows)};
   const size_t smem = size_t((a.group + 7) / 8 * 8) * (2 * p->d + 64 + 4);
+  const int pages = b->max_pages_per_seq;
+  if (pages <= kFuse || (pages <= 4 * kSelectThreads && rows >= kFuseRows)) {
+    return p->d == 64    ? launch(page_score_select_kernel<64, 4>, each, kSelectThreads, smem, stream, a)
+           : p->d == 128 ? launch(page_score_select_kernel<128, 4>, each, kSelectThreads, smem, stream, a)
+                         : launch(page_score_select_kernel<256, 4>, each, kSelectThreads, smem, stream, a);
+  }
   const attn_status_t scored = p->d == 64    ? launch(page_score_kernel<64>, grid, 128, smem, stream, a)
                                : p->d == 128 ? launch(page_score_kernel<128>, grid, 128, smem, stream, a)
                                              : launch(page_score_kernel<256>, grid, 128, smem, stream, a);
   if (scored != ATTN_OK) return scored;
-  const dim3 each{unsigned(rows)};
-  if (b->max_pages_per_seq <= 4 * kSelectThreads) return launch(page_select_kernel<4>, each, kSelectThreads, 0, stream, a);
-  if (b->max_pages_per_seq <= 16 * kSelectThreads) return launch(page_select_kernel<16>, each, kSelectThreads, 0, stream, a);
+  if (pages <= 4 * kSelectThreads) return launch(page_select_kernel<4>, each, kSelectThreads, 0, stream, a);
+  if (pages <= 16 * kSelectThreads) return launch(page_select_kernel<16>, each, kSelectThreads, 0, stream, a);
   return launch(page_select_kernel<0>, each, kSelectThreads, 0, stream, a);
 }
 

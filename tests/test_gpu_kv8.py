@@ -581,6 +581,27 @@ def test_select_row_lengths(pages):
         check_select(cache, q, table, [pages * page - 3], [1], k, 0, 1, 2, fwd=False)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("tokens,cap", [(1, 512), (1, 513), (13, 512), (12, 1024), (11, 1024), (12, 1025)])
+def test_select_rows_of_every_length_and_ties(d, tokens, cap):
+    # 8 heads: 96 rows and 512 pages are where one launch turns into two
+    page, rng = 16, np.random.default_rng(cap + tokens)
+    cache = H.make_cache(d, cap, 8, page, d)
+    table = np.stack([rng.permutation(cap) for _ in range(tokens)]).astype(np.int32)
+    pages = [cap, 1, 2, 15, 16, 17, 127, 128, 129, 255, 257, 300, 40][:tokens]
+    table[-1, 3::5] = -1
+    lens = [n * page - int(rng.integers(0, page)) for n in pages]
+    q = torch.randn(tokens, 24, d, generator=torch.Generator().manual_seed(cap)).to(bf16).cuda()
+    q[-1, :3] = 0                                                    # every score of one row 0: ties
+    for k in (3, 33):
+        check_select(cache, q, table, lens, [1] * tokens, k, 1, 1, 24, fwd=False)
+    # few different bounds, so scores agree in their leading digits or altogether
+    cache.k_bounds[:, :, :, 1:] = 0
+    cache.k_bounds[:, :, :, 0] = (cache.k_bounds[:, :, :, 0] // 16) * 16
+    cache.k_scale.fill_(0.25)
+    check_select(cache, q, table, lens, [1] * tokens, 33, 0, 2, 24, fwd=False)
+
+
 def test_select_full_mask_sees_every_token():
     cache = H.make_cache(4, 40, 2, 16, 64)
     table = H.make_table(9, [300, 200], 16, 40)
