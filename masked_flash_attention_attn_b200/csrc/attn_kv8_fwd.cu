@@ -677,27 +677,37 @@ __global__ void __launch_bounds__(32 * W, Cfg<D, NG, W>::CTAS) kv8_fwd_kernel(Fw
     if (!whole) {                                 // the last CTA of the item to arrive joins the parts
       const int fc = cta_of(item0 + lead), n = cta_of(item0 + length - 1) - fc + 1;
       __syncthreads();
-      if (tid == 0) {
-        __threadfence();                          // this CTA's part before its arrival
-        const uint32_t old = atomicAdd(a.counters + fc, 1u);
+      if (tid == 0) {                             // releases this CTA's part, acquires the others'
+        uint32_t old;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(a.counters + fc) : "memory");
         s_last = old == uint32_t(n - 1);
         if (s_last) a.counters[fc] = 0u;
       }
       __syncthreads();
       if (s_last) {
-        __threadfence();
         // parts at slots 2 c, but the first one's where it is not the start of its CTA's line
         const int odd = start_of(fc) >= item0 ? 0 : 1;
         const float2* pml = reinterpret_cast<const float2*>(a.part_ml) + int64_t(2 * fc) * ROWS;
         const float4* po = reinterpret_cast<const float4*>(a.part_o + int64_t(2 * fc) * (ROWS * D));
         // the 32 lanes of a warp (D = 64: each 16) hold one row: lane c the weight of part c
-        constexpr int PW = D == 64 ? 16 : 32, N = (ROWS * D / 4 + kThreads - 1) / kThreads;
+        // (the first P parts are on their way while the weights are worked out)
+        constexpr int PW = D == 64 ? 16 : 32, N = (ROWS * D / 4 + kThreads - 1) / kThreads, P = N <= 2 ? 8 / N : 1;
         float M[N], Z[N], w[N];
         float4 acc[N];
 #pragma unroll
         for (int k = 0; k < N; ++k) M[k] = kNone, Z[k] = 0.f, acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int b0 = 0; b0 < n; b0 += PW) {
           const int mc = b0 + (lane & (PW - 1)), nb = min(PW, n - b0);
+          auto part = [&](int c, int k) {
+            const int slot = b0 + c == 0 ? odd : 2 * (b0 + c);
+            return __ldcg(po + slot * (ROWS * D / 4) + min(ROWS * D / 4 - 1, tid + k * kThreads));
+          };
+          float4 early[P][N];
+#pragma unroll
+          for (int c = 0; c < P; ++c)
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+              if (c < nb) early[c][k] = part(c, k);
 #pragma unroll
           for (int k = 0; k < N; ++k) {
             const int r = min(ROWS - 1, (tid + k * kThreads) / (D / 4));
@@ -716,17 +726,20 @@ __global__ void __launch_bounds__(32 * W, Cfg<D, NG, W>::CTAS) kv8_fwd_kernel(Fw
             Z[k] = fmaf(Z[k], e0, zs);
             acc[k].x *= e0, acc[k].y *= e0, acc[k].z *= e0, acc[k].w *= e0;
           }
-#pragma unroll(N == 1 ? 8 : 4)
-          for (int c = 0; c < nb; ++c) {
-            const int slot = b0 + c == 0 ? odd : 2 * (b0 + c);
+          auto add = [&](int c, int k, const float4& v) {
+            const float e = __shfl_sync(~0u, w[k], c, PW);
+            acc[k].x = fmaf(e, v.x, acc[k].x), acc[k].y = fmaf(e, v.y, acc[k].y);
+            acc[k].z = fmaf(e, v.z, acc[k].z), acc[k].w = fmaf(e, v.w, acc[k].w);
+          };
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-              const float4 v = __ldcg(po + slot * (ROWS * D / 4) + min(ROWS * D / 4 - 1, tid + k * kThreads));
-              const float e = __shfl_sync(~0u, w[k], c, PW);
-              acc[k].x = fmaf(e, v.x, acc[k].x), acc[k].y = fmaf(e, v.y, acc[k].y);
-              acc[k].z = fmaf(e, v.z, acc[k].z), acc[k].w = fmaf(e, v.w, acc[k].w);
-            }
-          }
+          for (int c = 0; c < P; ++c)
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+              if (c < nb) add(c, k, early[c][k]);
+#pragma unroll(N == 1 ? 8 : 4)
+          for (int c = P; c < nb; ++c)
+#pragma unroll
+            for (int k = 0; k < N; ++k) add(c, k, part(c, k));
         }
 #pragma unroll
         for (int k = 0; k < N; ++k) {
