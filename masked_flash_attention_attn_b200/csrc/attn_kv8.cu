@@ -837,8 +837,10 @@ attn_status_t attn_page_tables(const attn_page_tables_t* t, attn_stream_t stream
   const int grid = std::min(148, (work + threads - 1) / threads);
   const size_t smem = size_t(3) * (t->batch + 1) * sizeof(int);
   if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
+      cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess) {
+    cudaGetLastError();
     return ATTN_ERR_CUDA;
+  }
   return launch(page_tables_kernel, dim3(grid), threads, smem, stream, *t, shift);
 }
 

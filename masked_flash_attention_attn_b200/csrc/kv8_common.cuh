@@ -177,7 +177,9 @@ inline attn_status_t launch(void (*kernel)(Params...), dim3 grid, int threads, s
   c.stream = reinterpret_cast<cudaStream_t>(stream);
   c.attrs = &at;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, kernel, args...) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  if (cudaLaunchKernelEx(&c, kernel, args...) == cudaSuccess) return ATTN_OK;
+  cudaGetLastError();             // the status says it; the caller's next check is not to find it again
+  return ATTN_ERR_CUDA;
 }
 
 inline Batch batch_of(const attn_kv8_plan_t* p, const attn_kv8_batch_t* b) {
