@@ -690,8 +690,10 @@ __global__ void __launch_bounds__(32 * W, Cfg<D, NG, W>::CTAS) kv8_fwd_kernel(Fw
         const float2* pml = reinterpret_cast<const float2*>(a.part_ml) + int64_t(2 * fc) * ROWS;
         const float4* po = reinterpret_cast<const float4*>(a.part_o + int64_t(2 * fc) * (ROWS * D));
         // the 32 lanes of a warp (D = 64: each 16) hold one row: lane c the weight of part c
-        // (the first P parts are on their way while the weights are worked out)
-        constexpr int PW = D == 64 ? 16 : 32, N = (ROWS * D / 4 + kThreads - 1) / kThreads, P = N <= 2 ? 8 / N : 1;
+        constexpr int PW = D == 64 ? 16 : 32, N = (ROWS * D / 4 + kThreads - 1) / kThreads;
+        // The first P parts are on their way while the weights are worked out. One at d = 256 (16 verifications:
+        // 48.8 us, 51.0 without), none in the tile of 32 rows, whose registers spill (96 rows of 32 requests: 203, 196)
+        constexpr int P = N <= 2 ? 8 / N : D == 256 ? 1 : 0;
         float M[N], Z[N], w[N];
         float4 acc[N];
 #pragma unroll
@@ -702,7 +704,7 @@ __global__ void __launch_bounds__(32 * W, Cfg<D, NG, W>::CTAS) kv8_fwd_kernel(Fw
             const int slot = b0 + c == 0 ? odd : 2 * (b0 + c);
             return __ldcg(po + slot * (ROWS * D / 4) + min(ROWS * D / 4 - 1, tid + k * kThreads));
           };
-          float4 early[P][N];
+          float4 early[P ? P : 1][N];
 #pragma unroll
           for (int c = 0; c < P; ++c)
 #pragma unroll
