@@ -34,6 +34,8 @@
 // piece are done at 28 us, with two at 36). Equal pieces handed out by a ticket measured slower at
 // any size. An item that several CTAs share is joined by the last of them to arrive (an atomic
 // counter that it resets), in the order of the keys: results do not depend on timing, nothing waits.
+// (One release-acquire atomic, and the join's first loads ahead of its weights, against two full fences
+// and loads behind them: 32 x 0.5-4 K tokens 39.7 -> 37.6 us.)
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
