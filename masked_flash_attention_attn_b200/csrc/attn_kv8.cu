@@ -715,7 +715,7 @@ __device__ __forceinline__ void pick_pages(int n, int k, int32_t* out, int (&s_h
     fixed |= 255u << shift;
     if (__shfl_sync(~0u, count, who) == rem) break;   // every key that matches is taken
   }
-  int eq0 = 0, gt0 = 0;           // counts before this round's pages
+  int eq0 = 0, gt0 = 0;           // counts before the current 256 pages
   each([&](int i, int p, uint32_t u) {
     if (i * kSelectThreads >= n) return;
     const bool gt = p < n && (u & fixed) > prefix, eq = p < n && (u & fixed) == prefix;
