@@ -212,6 +212,19 @@ __device__ __noinline__ uint32_t without_nan(uint32_t w, unsigned& top) {
   return (lo > 0x7f80u ? 0u : w & 0xffffu) | (hi > 0x7f80u ? 0u : w & 0xffff0000u);
 }
 
+// A channel's bounds (largest, smallest code in steps of 4) after its codes became RN(code * ratio). By powers of two codes
+// stay exact, or are subnormal and within one step, so scaling and rounding outwards is right. By
+// another ratio RN may go past bound * ratio (code 288, bound 72, ratio 0.95: code 288, 4 * 69 = 276): the
+// bound's own code is rounded as theirs were, and RN is monotone.
+__device__ __forceinline__ int2 grown_bounds(int hi, int lo, float ratio, bool exact) {
+  float h = float(hi) * ratio, l = float(lo) * ratio;
+  if (!exact) {
+    const float2 q = float2_of_e4m3(e4m3x4(float(4 * hi) * ratio, float(4 * lo) * ratio, 0.f, 0.f));
+    h = q.x * 0.25f, l = q.y * 0.25f;
+  }
+  return make_int2(__float2int_ru(h), __float2int_rd(l));
+}
+
 template <int NT, int NV>
 __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 8) append_kernel(AppendArgs a) {
   constexpr int kEnd = -2;        // slot of the tokens before the first and behind the last; -1: a skipped token
@@ -403,11 +416,13 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 8) append_kernel(AppendArg
       }
       __syncthreads();
       int8_t* b = a.bounds + block * (2 * D);
+      const bool exact = ratio == 1.f || ((__float_as_int(old) | __float_as_int(now)) & 0x7fffff) == 0;   // a power of two
       for (int c = tid; c < D; c += NT) {
         int hi = s_hi[c], lo = s_lo[c];
         if (off > 0) {
-          hi = max(hi, __float2int_ru(float(b[c]) * ratio));
-          lo = min(lo, __float2int_rd(float(b[D + c]) * ratio));
+          const int2 before = grown_bounds(b[c], b[D + c], ratio, exact);
+          hi = max(hi, before.x);
+          lo = min(lo, before.y);
         }
         b[c] = int8_t(hi);
         b[D + c] = int8_t(lo);

@@ -94,8 +94,11 @@ def append(codes, scale, bounds, x, slots, page):
                 q = new / 4
                 hi, lo = np.ceil(q).max(0), np.floor(q).min(0)
                 if off:
-                    hi = np.maximum(hi, np.ceil(bounds[pg, h, 0] * ratio))
-                    lo = np.minimum(lo, np.floor(bounds[pg, h, 1] * ratio))
+                    before = bounds[pg, h] * ratio
+                    if math.frexp(was)[0] not in (0.0, 0.5) and ratio < 1:    # codes may have been rounded away from zero
+                        before = e4m3_round(4.0 * before) / 4
+                    hi = np.maximum(hi, np.ceil(before[0]))
+                    lo = np.minimum(lo, np.floor(before[1]))
                 bounds[pg, h] = np.stack([hi, lo])
             scale[pg, h] = np.nan if nan else now
     return codes, scale, bounds

@@ -208,6 +208,34 @@ def test_append_token_by_token_equals_one_call():
     assert torch.equal(one.v.view(torch.uint8), many.v.view(torch.uint8))
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_append_bounds_hold_the_codes_when_any_scale_grows(d):
+    # a caller's scales, growing by any factor: the bounds against the codes themselves
+    page, hkv, pages = 16, 3, 60
+    cache = H.make_cache(d, pages, hkv, page, d, 0, 0)
+    g = torch.Generator().manual_seed(d)
+    ratio = torch.rand(pages, hkv, generator=g) * 0.97 + 0.02
+    ratio[0], ratio[1], ratio[2] = 0.95, 0.6093, 0.5          # codes 288 and 224 are rounded up by the first two
+    cache.k_scale.copy_(ratio.cuda())
+    k = torch.randn(pages * hkv * page * d, generator=g).mul(120).clamp(-448, 448).view(pages, hkv, page, d)
+    k[:, :, :, 2], k[:, :, :, 3], k[:, :, :, 4], k[:, :, :, 5] = 288, 224, -288, -224
+    cache.k.copy_(k.to(H.E4M3).cuda())
+    x = cache.k.float()
+    cache.k_bounds.copy_(torch.stack([torch.ceil(x.amax(2) / 4), torch.floor(x.amin(2) / 4)], 2).to(torch.int8))
+    new = torch.zeros(pages, hkv, d, dtype=bf16, device="cuda")
+    new[:, :, 7] = 448                                        # needs a scale of 1
+    before = H.values(cache.k)                                # the bounds are of all its places
+    M.attn_kv8_append(cache, new, new, H.i32(np.arange(pages) * page + page - 1))
+    assert (cache.k_scale == 1).all()
+    codes, b = H.values(cache.k), cache.k_bounds.cpu().numpy().astype(int)
+    assert (4 * b[:, :, 0] >= codes.max(2)).all() and (4 * b[:, :, 1] <= codes.min(2)).all()
+    # and no wider: 3 codes from the outward rounding of the old bound, half a step (2^-4) of the format, 4 codes of the new
+    r = ratio.numpy()[:, :, None]
+    top, low = np.maximum(before.max(2) * r, 0), np.minimum(before.min(2) * r, 0)
+    assert (4 * b[:, :, 0] <= np.maximum((top + 3) * (1 + 2.0 ** -4) + 4.01, codes.max(2))).all()
+    assert (4 * b[:, :, 1] >= np.minimum((low - 3) * (1 + 2.0 ** -4) - 4.01, codes.min(2))).all()
+
+
 def test_append_without_bounds_and_empty():
     cache = M.Kv8Cache(4, page_size=16, hkv=2, head_dim=64, bounds=False)
     k, v = draw_kv(1, 5, 2, 64)

@@ -62,6 +62,22 @@ def test_selection_oracle_bounds_the_logits():
     assert sel[0, 0, 0] == 0 and sel[0, 0, -1] == pages - 1 and (np.diff(sel[0, 0]) > 0).all()
 
 
+def test_append_oracle_bounds_hold_the_codes_when_any_scale_grows():
+    rng = np.random.default_rng(5)
+    page, d = 16, 64
+    for ratio in np.concatenate([rng.uniform(0.02, 1, 40), np.exp2(-np.arange(12.0)), [0.95, 0.6093]]):
+        codes = O.e4m3_round(rng.normal(size=(1, 1, page, d)) * 120)
+        codes[0, 0, 3, 0], codes[0, 0, 4, 1] = 288, -288
+        codes[0, 0, :, 2], codes[0, 0, :, 3] = 288, 224
+        bounds = np.stack([np.ceil(codes.max(2) / 4), np.floor(codes.min(2) / 4)], 2)
+        x = np.zeros((1, 1, d))
+        x[0, 0, -1] = 448                                 # the new scale is 1, the one before `ratio`
+        got, scale, b = O.append(codes, np.full((1, 1), ratio), bounds, x, [page - 1], page)
+        old = got[0, 0, :page - 1]
+        assert scale[0, 0] == 1 and np.array_equal(old, O.e4m3_round(codes[0, 0, :page - 1] * ratio))
+        assert (4 * b[0, 0, 0] >= got[0, 0].max(0)).all() and (4 * b[0, 0, 1] <= got[0, 0].min(0)).all(), ratio
+
+
 def test_attention_oracle_against_torch():
     rng = np.random.default_rng(2)
     q, k, v = rng.normal(size=8), rng.normal(size=(20, 8)), rng.normal(size=(20, 8))
