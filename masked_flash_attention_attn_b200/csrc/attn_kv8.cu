@@ -21,6 +21,8 @@ namespace {
 // occupied part are read, entries from the old page count on and the ring's empty part written).
 struct Sums { long long tok; int take, give; };
 
+constexpr int kMaxBatch = 16384;  // 3 prefixes of it in shared memory: 192 KiB
+
 __device__ __forceinline__ int pages_of(int n, int shift) { return int((unsigned(n) + (1u << shift) - 1) >> shift); }
 
 __device__ __forceinline__ Sums add(Sums a, Sums b) { return Sums{a.tok + b.tok, a.take + b.take, a.give + b.give}; }
@@ -829,7 +831,7 @@ extern "C" {
 attn_status_t attn_page_tables(const attn_page_tables_t* t, attn_stream_t stream) {
   if (!t) return ATTN_ERR_INVALID_ARG;
   const int shift = shift_of(t->page_size);
-  if (shift < 0 || t->batch > 16384) return ATTN_ERR_UNSUPPORTED;
+  if (shift < 0 || t->batch > kMaxBatch) return ATTN_ERR_UNSUPPORTED;
   if (t->batch < 0 || t->max_pages_per_seq < 1 || t->num_pages < 1 || t->max_tokens < 0) return ATTN_ERR_INVALID_ARG;
   if (int64_t(t->batch) * t->max_pages_per_seq >= (int64_t(1) << 31) ||
       int64_t(t->num_pages) * t->page_size >= (int64_t(1) << 31))
@@ -851,8 +853,10 @@ attn_status_t attn_page_tables(const attn_page_tables_t* t, attn_stream_t stream
   const int threads = work <= 256 ? 256 : 1024;
   const int grid = std::min(148, (work + threads - 1) / threads);
   const size_t smem = size_t(3) * (t->batch + 1) * sizeof(int);
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess) {
+  // The 48 KiB that need no opt-in hold the kernel's static arrays too. Always the same maximum, that of the
+  // largest batch, so that a call never takes back what another thread's launch needs.
+  if (smem > 32 * 1024 && cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               int(3 * (kMaxBatch + 1) * sizeof(int))) != cudaSuccess) {
     cudaGetLastError();
     return ATTN_ERR_CUDA;
   }

@@ -1,6 +1,10 @@
 """The 8-bit paged K/V cache on the GPU against its 64-bit oracle (oracle/kv8.py): page
 tables, append and page selection exactly, attention within the bound of
 kv8_helpers.check_rows, and a run of them together."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -65,6 +69,17 @@ def test_tables_match_the_oracle(batch, page, width):
     assert ref[2][2] == 0
     check_tables(table, old, new, ring, state, page, tokens, positions=False)
     check_tables(table, old, new, ring, state, page, tokens + 3, repeat=3)     # a repeated call gives the same
+
+
+def test_tables_batches_around_48_kib_of_prefixes_in_a_new_process():
+    # 12 bytes a request and the kernel's static shared memory; in a process in which no larger batch ran before
+    code = ("from tests.test_gpu_kv8 import check_tables, tables_problem\n"
+            "for batch in (2729, 2730, 4051, 4052, 4095, 4096, 16384, 4052):\n"
+            "    t, old, new, ring, state, tokens = tables_problem(batch, batch, 16, 3)\n"
+            "    check_tables(t, old, new, ring, state, 16, tokens)\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_tables_refuse_on_the_device_and_still_shrink():
