@@ -214,21 +214,22 @@ __device__ __noinline__ uint32_t without_nan(uint32_t w, unsigned& top) {
   return (lo > 0x7f80u ? 0u : w & 0xffffu) | (hi > 0x7f80u ? 0u : w & 0xffff0000u);
 }
 
-// A channel's bounds (largest, smallest code in steps of 4) after its codes became RN(code * ratio). By powers of two codes
-// stay exact, or are subnormal and within one step, so scaling and rounding outwards is right. By
-// another ratio RN may go past bound * ratio (code 288, bound 72, ratio 0.95: code 288, 4 * 69 = 276): the
-// bound's own code is rounded as theirs were, and RN is monotone.
-__device__ __forceinline__ int2 grown_bounds(int hi, int lo, float ratio, bool exact) {
-  float h = float(hi) * ratio, l = float(lo) * ratio;
-  if (!exact) {
-    const float2 q = float2_of_e4m3(e4m3x4(float(4 * hi) * ratio, float(4 * lo) * ratio, 0.f, 0.f));
-    h = q.x * 0.25f, l = q.y * 0.25f;
+// Bounds (largest, smallest code of a channel in steps of 4) after the codes became RN(code * ratio). By powers of two codes
+// stay exact, or are subnormal and within one step, so scaling and rounding outwards is right. By another
+// ratio RN may go past bound * ratio (code 288, bound 72, ratio 0.95: code 288, 4 * 69 = 276): here the
+// bound's own code is rounded as theirs were, and RN is monotone. Only for scales that a caller chose: out of line.
+__device__ __noinline__ void round_bounds(int8_t* b, int d, float ratio) {
+  for (int c = threadIdx.x; c < d; c += blockDim.x) {
+    const float2 q = float2_of_e4m3(e4m3x4(float(4 * b[c]) * ratio, float(4 * b[d + c]) * ratio, 0.f, 0.f));
+    b[c] = int8_t(__float2int_ru(q.x * 0.25f));
+    b[d + c] = int8_t(__float2int_rd(q.y * 0.25f));
   }
-  return make_int2(__float2int_ru(h), __float2int_rd(l));
 }
 
+// CTAs per SM: 9 where a page is few vectors (56 registers; 10.8 K tokens of 8 x 128 in pages of 16 take 34.9 us, 37.7
+// with 64 registers and 8 CTAs), 8 and 2 for larger pages, whose values fill the registers.
 template <int NT, int NV>
-__global__ void __launch_bounds__(NT, NT == 256 ? 2 : 8) append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(NT, NT == 256 ? 2 : NV <= 2 ? 9 : 8) append_kernel(AppendArgs a) {
   constexpr int kEnd = -2;        // slot of the tokens before the first and behind the last; -1: a skipped token
   __shared__ int s_slot[260];     // of the tokens t0 - 1 .. t0 + span + page_size - 1
   __shared__ int s_list[128];
@@ -347,7 +348,12 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 8) append_kernel(AppendArg
     const float unit = __int_as_float((e + 127) << 23), now = nan ? unit : fmaxf(old, unit);
     const float ratio = nan ? 1.f : old / now;
     uint8_t* codes = (is_v ? a.codes[1] : a.codes[0]) + block * (int64_t(ps) * D);
+    float bound_ratio = ratio;
     if (off > 0 && ratio < 1.f) { // the codes before, in the new unit
+      if (bound && (__float_as_int(old) & 0x7fffff)) {    // not a power of two (the loop below has the same channels per thread)
+        round_bounds(a.bounds + block * (2 * D), D, ratio);
+        bound_ratio = 1.f;
+      }
       for (int v = tid; v < off * D / 16; v += NT) {
         uint4* p = reinterpret_cast<uint4*>(codes) + v;
         const uint4 c = *p;
@@ -418,13 +424,11 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 8) append_kernel(AppendArg
       }
       __syncthreads();
       int8_t* b = a.bounds + block * (2 * D);
-      const bool exact = ratio == 1.f || ((__float_as_int(old) | __float_as_int(now)) & 0x7fffff) == 0;   // a power of two
       for (int c = tid; c < D; c += NT) {
         int hi = s_hi[c], lo = s_lo[c];
         if (off > 0) {
-          const int2 before = grown_bounds(b[c], b[D + c], ratio, exact);
-          hi = max(hi, before.x);
-          lo = min(lo, before.y);
+          hi = max(hi, __float2int_ru(float(b[c]) * bound_ratio));
+          lo = min(lo, __float2int_rd(float(b[D + c]) * bound_ratio));
         }
         b[c] = int8_t(hi);
         b[D + c] = int8_t(lo);
