@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <cstdint>
 
 #include "kv8_common.cuh"
@@ -226,6 +227,75 @@ __device__ __noinline__ void round_bounds(int8_t* b, int d, float ratio) {
   }
 }
 
+// The nearest token at or behind t (forward) or at or before it that is not skipped, -1 if there is none; by the
+// whole CTA, 8 slots a thread and one barrier a round (16 slots: no faster, and the kernel's registers spill). A captured step
+// passes all of its slots, the last of them -1, and tokens that are cached already may be left out in front, so
+// runs end and start at such stretches. In a graph, 8 heads of d = 128: 32 tokens in 8192 slots 20.9 us, 18.7 of them for the
+// empty CTAs (39.4 us by windows of NT slots and four barriers); behind 8192 skipped slots 21.5 (371 by a walk of one thread).
+template <int NT, bool FORWARD>
+__device__ __noinline__ int nearest_token(const int32_t* slots, int64_t t, int tokens, unsigned num_slots, int* s_found) {
+  constexpr int PER = 8;
+  for (int64_t at = t; FORWARD ? at < tokens : at >= 0; at += FORWARD ? NT * PER : -NT * PER) {
+    const int left = int(min(FORWARD ? tokens - at : at + 1, int64_t(NT * PER)));
+    const int32_t* from = slots + at;
+    int s[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {             // without branches, so that the loads overlap
+      const int w = min(i * NT + int(threadIdx.x), left - 1);
+      s[i] = from[FORWARD ? w : -w];
+    }
+    int dist = INT_MAX;           // from `at`
+#pragma unroll
+    for (int i = PER - 1; i >= 0; --i) {
+      const int w = i * NT + threadIdx.x;
+      if (w < left && unsigned(s[i]) < num_slots) dist = w;
+    }
+    if (!__syncthreads_or(dist < INT_MAX)) continue;
+    dist = __reduce_min_sync(~0u, dist);
+    if ((threadIdx.x & 31) == 0) s_found[threadIdx.x >> 5] = dist;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) dist = min(dist, s_found[i]);
+    return int(FORWARD ? at + dist : at - dist);
+  }
+  return -1;
+}
+
+// Tokens t .. t + n - 1 hold consecutive places and a skipped token or place follows: lists the run's tokens, up
+// to the first of another page, and returns their number; 0 if the n are all.
+template <int NT>
+__device__ __noinline__ int list_run(const int32_t* slots, int tokens, unsigned num_slots, int shift, int t, int n, int2* s_run,
+                                     int& s_stop, int* s_taken) {
+  const int tid = threadIdx.x, ps = 1 << shift, pg = slots[t] >> shift;
+  const int64_t next = nearest_token<NT, true>(slots, int64_t(t) + n, tokens, num_slots, s_taken);
+  if (next < 0 || (slots[next] >> shift) != pg) return 0;
+  n = 0;
+  for (int64_t w0 = t; w0 >= 0; w0 = nearest_token<NT, true>(slots, w0 + NT, tokens, num_slots, s_taken)) {
+    __syncthreads();
+    if (tid == 0) s_stop = NT;
+    __syncthreads();
+    const int64_t w = w0 + tid;
+    const int s = w < tokens ? slots[w] : 0;
+    const bool valid = w < tokens && unsigned(s) < num_slots;
+    if (w >= tokens || (valid && (s >> shift) != pg)) atomicMin(&s_stop, tid);
+    __syncthreads();
+    const int stop = s_stop;
+    const bool take = valid && tid < stop;
+    const unsigned m = __ballot_sync(~0u, take);
+    if ((tid & 31) == 0) s_taken[tid >> 5] = __popc(m);
+    __syncthreads();
+    int at = n + __popc(m & ((1u << (tid & 31)) - 1u));
+    for (int i = 0; i < NT / 32; ++i) {
+      if (i < (tid >> 5)) at += s_taken[i];
+      n += s_taken[i];
+    }
+    if (take && at < ps) s_run[at] = make_int2(int(w), s & (ps - 1));
+    if (stop < NT || n >= ps) break;
+  }
+  __syncthreads();
+  return min(n, ps);
+}
+
 // CTAs per SM: 9 where a page is few vectors (56 registers; 10.8 K tokens of 8 x 128 in pages of 16 take 34.9 us, 37.7
 // with 64 registers and 8 CTAs), 8 and 2 for larger pages, whose values fill the registers.
 template <int NT, int NV>
@@ -252,9 +322,20 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NV <= 2 ? 9 : 8) append_ke
     s_slot[j] = valid(s) ? s : t >= 0 && t < a.tokens ? -1 : kEnd;
   }
   __syncthreads();
-  if (tid < a.span && valid(s_slot[tid + 1])) {
-    int before = s_slot[tid];     // a run starts where the token before (skipped ones aside) is of another page
-    for (int t = t0 + tid - 2; t >= 0 && !valid(before); --t) before = a.slots[t];
+  const bool live = tid < a.span && valid(s_slot[tid + 1]);
+  int outside = s_slot[0];        // of the last token in front of the CTA's, skipped ones aside
+  if (outside == -1) {
+    if (!__syncthreads_or(live)) return;
+    const int t = nearest_token<NT, false>(a.slots, int64_t(t0) - 2, a.tokens, a.num_slots, s_taken);
+    if (t >= 0) outside = a.slots[t];
+  }
+  if (live) {                     // a run starts where the token before is of another page
+    int before = s_slot[tid];
+    if (before == -1) {
+      int j = tid;
+      while (j > 0 && s_slot[j] == -1) --j;
+      before = j > 0 ? s_slot[j] : outside;
+    }
     if (!valid(before) || (before >> a.shift) != (s_slot[tid + 1] >> a.shift)) s_list[atomicAdd(&s_count, 1)] = tid;
   }
   __syncthreads();
@@ -267,31 +348,11 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 2 : NV <= 2 ? 9 : 8) append_ke
     if (tid < ps - off && s_slot[j0 + tid] != s0 + tid) atomicMin(&s_stop, tid);
     __syncthreads();
     int n = s_stop;               // tokens in consecutive places
-    const bool whole = n == ps - off || s_slot[j0 + n] == kEnd || (valid(s_slot[j0 + n]) && (s_slot[j0 + n] >> a.shift) != pg);
-    if (!whole) {                 // places or tokens are left out: list the run's tokens, up to the first of another page
-      n = 0;
-      for (int w0 = t;; w0 += NT) {
-        __syncthreads();
-        if (tid == 0) s_stop = NT;
-        __syncthreads();
-        const int w = w0 + tid, s = w < a.tokens ? a.slots[w] : kEnd;
-        if (w >= a.tokens || (valid(s) && (s >> a.shift) != pg)) atomicMin(&s_stop, tid);
-        __syncthreads();
-        const int stop = s_stop;
-        const bool take = valid(s) && tid < stop;
-        const unsigned m = __ballot_sync(~0u, take);
-        if ((tid & 31) == 0) s_taken[tid >> 5] = __popc(m);
-        __syncthreads();
-        int at = n + __popc(m & ((1u << (tid & 31)) - 1u));
-        for (int i = 0; i < NT / 32; ++i) {
-          if (i < (tid >> 5)) at += s_taken[i];
-          n += s_taken[i];
-        }
-        if (take && at < ps) s_run[at] = make_int2(w, s & (ps - 1));
-        if (stop < NT || n >= ps) break;
-      }
-      n = min(n, ps);
-      __syncthreads();
+    bool whole = n == ps - off || s_slot[j0 + n] == kEnd || (valid(s_slot[j0 + n]) && (s_slot[j0 + n] >> a.shift) != pg);
+    if (!whole) {
+      const int listed = list_run<NT>(a.slots, a.tokens, a.num_slots, a.shift, t, n, s_run, s_stop, s_taken);
+      whole = listed == 0;
+      n = whole ? n : listed;
     }
     const int vecs = n << vshift;
     if (bound)

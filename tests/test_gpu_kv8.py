@@ -176,6 +176,43 @@ def test_append_strided_views_and_skipped_slots():
     check_append(cache, k, v, slots, page)
 
 
+@pytest.mark.parametrize("page,d", [(16, 64), (64, 64), (128, 64), (64, 256), (128, 256)])
+@pytest.mark.parametrize("gap", [1, 31, 128, 2047, 2048, 2049, 5000])
+def test_append_between_stretches_of_skipped_slots(page, d, gap):
+    # skipped in front, inside a page's tokens, between pages and behind the last token, as a padded step has them
+    table = H.make_table(gap, [page + 7, 2 * page + 3, 40], page, 12)
+    first, second, third = (slots_for(table[b:b + 1], [o], [n], page) for b, (o, n) in enumerate([(3, page + 4), (0, 2 * page + 3), (33, 7)]))
+    skip = [-1] * gap
+    for slots in ([skip, first, skip, second, third, skip], [first[:5], skip, first[5:9], skip, first[9:], second[:-1], skip, second[-1:], skip],
+                  [first, second, third[:1], skip, third[1:2], skip, third[2:], [12 * page, -2], skip], [skip, [-2 ** 31, 2 ** 31 - 1]]):
+        slots = np.concatenate([np.asarray(x, np.int32) for x in slots])
+        cache = H.make_cache(page + d, 12, 1, page, d, -14, -9)
+        k, v = draw_kv(gap, len(slots), 1, d)
+        check_append(cache, k, v, slots, page)
+
+
+def test_append_passes_long_stretches_of_skipped_slots_quickly():
+    # 65536 slots of a captured step with 32 tokens in use. A thread that walks over the skipped slots before a token
+    # one by one takes about 3 ms, a CTA that lists those behind a page's last token 130 slots at a time 0.17 ms
+    cache = M.Kv8Cache(128, page_size=16, hkv=8, head_dim=128)
+    k = torch.zeros(65536, 8, 128, dtype=bf16, device="cuda")
+
+    def shortest(slots):
+        s, times = H.i32(slots), []
+        for _ in range(9):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            M.attn_kv8_append(cache, k, k, s)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+    part, full = np.arange(32) * 16 + 48, np.arange(32) * 16 + 63
+    skip = np.full(65536 - 32, -1)
+    assert shortest(np.concatenate([skip, part])) < 1.0
+    assert shortest(np.concatenate([part, skip])) - shortest(np.concatenate([full, skip])) < 0.08
+
+
 def test_append_special_values():
     page, hkv, d = 16, 1, 64
     cache = H.make_cache(7, 12, hkv, page, d)
