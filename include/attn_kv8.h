@@ -160,8 +160,9 @@ typedef struct {
  * [total_q][hkv][n_selected], as attn_kv8_select() writes it) token t of KV head h sees only keys of the listed
  * pages (numbers of page_table columns; the first min(n_selected, pages it sees) entries are
  * read, a negative or too large one sees nothing; a page listed twice counts twice); the plan's
- * mask applies within them. Products are exact and sums fp32; P is rounded to fp16 relative to
- * the row's running maximum. Results do not depend on timing (partial results are
+ * mask applies within them. Products are exact and sums fp32 (q values below 2^-31 of their row's
+ * largest, or below 2^-117, lose bits); P is rounded to fp16, by 2^-11 of the largest P of its 16 keys at most, for keys up to
+ * 65 nats below the row's maximum. Results do not depend on timing (partial results are
  * joined in a fixed order).
  * Errors: INVALID_ARG (also: another device is current than the plan's, a cache of another shape
  * than the plan's), CUDA. */

@@ -3,8 +3,8 @@
 // Mathematics. Per request, KV head h and query row n (a token and a query head of h's group):
 //     s_j = scale k_scale[page(j)] (q_n . code_j),  p_j = 2^(s_j log2 e - m_n),
 //     out = sum_j p_j v_scale[page(j)] code_j / sum_j p_j,  lse = m_n ln 2 + ln sum_j p_j
-// with the running maximum m_n. e4m3 codes convert to fp16 exactly and q is scaled by a power of
-// two per row into fp16 range, so the products are exact; both matrix products run on
+// with m_n near the running maximum. e4m3 codes convert to fp16 exactly and q is scaled by a power of
+// two per row into fp16 range, so the products are exact (of q values from 2^-31 of the row's largest on); both matrix products run on
 // mma.sync m16n8k16 with fp32 accumulators, transposed: S^T = K Q^T and O^T = V^T P^T, keys or
 // channels on the 16-row side and 8 query rows on the other, so the eight rows of a grouped
 // decode step fill a tile (as the 128-row side of a tcgen05 MMA they would use 6 % of it).
@@ -55,8 +55,16 @@ constexpr int kStep = 16;                 // keys per step
 constexpr int kStart = 3;                 // chunks that starting on an item is worth in the line
 constexpr int kPiece = 6;                 // chunks over the mean that one piece each may take
 constexpr int kTries = 8;                 // lengths of a piece that are tried, 1/16 of the mean apart
-constexpr float kNone = -3.402823466e38f;  // running maximum of a row that has seen no key; finite, so differences are never NaN
-constexpr float kLazy = 8.f;              // log2 units a score may exceed the running maximum by
+constexpr float kNone = -3.402823466e38f;  // reference of a row that has seen no key; finite, so differences are never NaN
+// P is 2^(s - m) in fp16, m the row's reference. When P of a step's largest key would leave 2^(+-kRange), m moves to kHead
+// below that key, down as well as up: fp16 keeps 11 bits down to 2^-14, so the rounding of a P is at most 2^-11 of the
+// largest of its 16 keys, however far those are below the row's maximum. (With the running maximum as reference,
+// keys 17 nats below a sink lost a third of their sum.) Downwards until the row's sum is 2^kGrow, far from the
+// end of fp32 for the products too: keys up to 65 nats below the maximum.
+// (16 verifications at d = 256: 47.1 us with the maximum as reference, 48.3 so; decode steps within 1 %.)
+constexpr float kHead = 6.f;
+constexpr float kRange = 14.f;
+constexpr int kGrow = 80;
 
 struct FwdArgs {
   Batch b;
@@ -509,7 +517,7 @@ __global__ void __launch_bounds__(32 * W, Cfg<D, NG, W>::CTAS) kv8_fwd_kernel(Fw
       // scores in log2 units, masked; accumulator rows are keys key + g and key + g + 8
       const float ks = scale.x, vs = scale.y;
       const bool partial = key + kStep > hi_all || key < lo_all;
-      bool over = false;
+      bool out_of_range = false;                  // of a lane's two keys: it may be only these
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
 #pragma unroll
@@ -523,9 +531,9 @@ __global__ void __launch_bounds__(32 * W, Cfg<D, NG, W>::CTAS) kv8_fwd_kernel(Fw
             if (key + g + 8 >= hi || key + g + 8 < lo) s[n][c + 2] = -INFINITY;
           }
         }
-        over |= fmaxf(s[n][0], s[n][2]) > m[n][0] + kLazy || fmaxf(s[n][1], s[n][3]) > m[n][1] + kLazy;
+        out_of_range |= fabsf(fmaxf(s[n][0], s[n][2]) - m[n][0]) > kRange || fabsf(fmaxf(s[n][1], s[n][3]) - m[n][1]) > kRange;
       }
-      if (__any_sync(~0u, over)) {                // raise the maxima and rescale
+      if (__any_sync(~0u, out_of_range)) {        // move the references and rescale
 #pragma unroll
         for (int n = 0; n < NG; ++n)
 #pragma unroll
@@ -534,9 +542,16 @@ __global__ void __launch_bounds__(32 * W, Cfg<D, NG, W>::CTAS) kv8_fwd_kernel(Fw
             x2 = fmaxf(x2, __shfl_xor_sync(~0u, x2, 4));
             x2 = fmaxf(x2, __shfl_xor_sync(~0u, x2, 8));
             x2 = fmaxf(x2, __shfl_xor_sync(~0u, x2, 16));
-            if (x2 > m[n][c]) {
-              const float r = ex2(m[n][c] - x2);
-              m[n][c] = x2;
+            float sum = l[n][c];
+            sum += __shfl_xor_sync(~0u, sum, 4);
+            sum += __shfl_xor_sync(~0u, sum, 8);
+            sum += __shfl_xor_sync(~0u, sum, 16);
+            const bool low = x2 < m[n][c] - kRange && x2 > -INFINITY;
+            float to = x2 - kHead;
+            if (low) to = fmaxf(to, m[n][c] - max(0, kGrow - ((__float_as_int(sum) >> 23) - 127)));
+            if (low || to > m[n][c]) {
+              const float r = ex2(m[n][c] - to);
+              m[n][c] = to;
               l[n][c] *= r;
 #pragma unroll
               for (int j = 0; j < D / 16; ++j) {

@@ -442,6 +442,52 @@ def test_scores_that_rise_along_the_keys_and_wide_scales():
     attend(2, [317], [1], hq=4, hkv=1, d=d, page=page, cache=cache, table=table, q=torch.full((1, 4, d), -1.0, dtype=bf16, device="cuda"))
 
 
+@pytest.mark.parametrize("at", ["first", "middle", "last"])
+@pytest.mark.parametrize("d,hq,tokens,many", [(64, 8, 1, False), (128, 8, 1, False), (256, 8, 1, False), (128, 16, 1, False), (64, 8, 4, False),
+                                              (128, 8, 4, False), (256, 8, 2, False), (128, 8, 1, True), (64, 16, 1, True), (256, 8, 2, True)])
+def test_keys_far_below_one_that_dominates(d, hq, tokens, many, at):
+    # one key 0 .. 60 nats above the others (each head another gap), its value 0: all of the output is the others'.
+    # Requests share their pages, so that there are enough of them for a warp to have a large part of a request's keys.
+    # Bound: a P is off by 2^-11 of the largest p of its 16 keys or by itself, exponents by the fp32 score sum and ex2, sums
+    # over n keys, the result to bf16 (as in kv8_helpers.check_rows, but without its absolute term)
+    page, n = 16, 3000
+    batch = 1300 if many else 600
+    cache = H.make_cache(d, n // page + 5, 1, page, d)
+    table = H.make_table(d, [n], page, cache.num_pages)
+    star = {"first": 0, "middle": 1501, "last": n - tokens}[at]
+    k, v = cache.k.view(torch.uint8), cache.v.view(torch.uint8)
+    k[:, :, :, 0] = 0
+    k[table[0, star // page], 0, star % page] = 0
+    k[table[0, star // page], 0, star % page, 0] = 0x7E                        # 448
+    v[table[0, star // page], 0, star % page] = 0
+    cache.k_scale.fill_(2.0 ** -8)
+    q = torch.randn(tokens, hq, d, generator=torch.Generator().manual_seed(d))
+    gap = torch.tensor([0, 8, 12, 14, 17, 21, 30, 60.0])[torch.arange(hq) % 8]
+    q[:, :, 0] = gap / (d ** -0.5 * 448 * 2.0 ** -8)
+    q = q.to(bf16).cuda()
+    plan = M.attn_kv8_plan(hq=hq, hkv=1, head_dim=d, page_size=page, mask=masks.causal(), max_q_len=tokens)
+    out, lse = M.forward_kv8(plan, cache, q.repeat(batch, 1, 1), H.i32(np.repeat(table, batch, 0)), H.i32([n] * batch),
+                             H.i32(H.cu_of([tokens] * batch)))
+    out, lse = out.view(batch, tokens, hq, d), lse.view(batch, tokens, hq)
+    kk, vv = H.Keys(cache).of(table[0], n, 0)
+    for t in range(tokens):
+        hi = n - tokens + t + 1
+        step = np.arange(0, hi, 16)
+        va = np.abs(vv[:hi])
+        for a in range(hq):
+            qa = q[t, a].double().cpu().numpy()
+            s = kk[:hi] @ qa * d ** -0.5
+            p = np.exp(s - s.max())
+            z, ref = p.sum(), p @ vv[:hi]
+            top = np.repeat(np.maximum.reduceat(p, step), 16)[:hi]
+            dp = (d + 4) * 2.0 ** -24 * (np.abs(kk[:hi]) @ np.abs(qa)).max() * d ** -0.5 + 2.0 ** -21
+            tol = np.minimum(p, 2.0 ** -11 * top) @ va + (2 * dp + (hi + 64) * 2.0 ** -23) * (p @ va) + 2.0 ** -8 * np.abs(ref)
+            for b in (0, batch // 2, batch - 1):
+                err = np.abs(out[b, t, a].double().cpu().numpy() - ref / z)
+                assert (err <= tol / z).all(), (b, t, a, float(gap[a]), float((err * z / tol).max()), float(err.max() * z / np.abs(ref).max()))
+                assert abs(float(lse[b, t, a]) - (s.max() + np.log(z))) <= dp + (hi + 64) * 2.0 ** -23 + abs(s.max()) * 2.0 ** -22
+
+
 @pytest.mark.parametrize("mag", [1e-30, 2.0 ** -20, 300.0, 1e30])
 def test_query_magnitudes(mag):
     cache = H.make_cache(4, 20, 2, 16, 64)
