@@ -115,7 +115,8 @@ attn_status_t attn_kv8_append(const attn_kv8_cache_t* cache, const void* k_new, 
  * k_out, v_out (bf16 [total_k][hkv][head_dim], 16-byte aligned) is token j of request b. Values
  * code * scale are rounded to bf16 (exact for power-of-two scales, as attn_kv8_append() writes).
  * cu_seqlens_k: DEVICE int32 [batch + 1], non-decreasing from 0; rows from cu_seqlens_k[batch] on
- * are left as they were. page_table: DEVICE int32 [batch][max_pages_per_seq].
+ * are left as they were. page_table: DEVICE int32 [batch][max_pages_per_seq]; tokens past its
+ * max_pages_per_seq pages are zeros, as those of pages outside the cache.
  * Errors: INVALID_ARG, UNSUPPORTED (page_size, head_dim), CUDA. */
 attn_status_t attn_kv8_gather(const attn_kv8_cache_t* cache, const int32_t* page_table, int32_t max_pages_per_seq,
                               const int32_t* cu_seqlens_k, int32_t batch, int64_t total_k, void* k_out, void* v_out,

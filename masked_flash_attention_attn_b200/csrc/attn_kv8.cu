@@ -532,8 +532,8 @@ __global__ void __launch_bounds__(256) gather_kernel(GatherArgs a) {
       }
       const int64_t j = row - a.cu_k[x];
       const int64_t pi = j >> a.shift;
-      if (j >= 0 && row < a.cu_k[x + 1] && pi < a.max_pages) {
-        pg = a.page_table[int64_t(x) * a.max_pages + pi];
+      if (j >= 0 && row < a.cu_k[x + 1]) {      // tokens past the table's row are zeros, as those of pages outside the cache
+        pg = pi < a.max_pages ? a.page_table[int64_t(x) * a.max_pages + pi] : -1;
         if (unsigned(pg) >= unsigned(a.num_pages)) pg = -1;
         off = int(j) & ((1 << a.shift) - 1);
       }

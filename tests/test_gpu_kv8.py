@@ -442,7 +442,7 @@ def test_scores_that_rise_along_the_keys_and_wide_scales():
     attend(2, [317], [1], hq=4, hkv=1, d=d, page=page, cache=cache, table=table, q=torch.full((1, 4, d), -1.0, dtype=bf16, device="cuda"))
 
 
-@pytest.mark.parametrize("at", ["first", "middle", "last"])
+@pytest.mark.parametrize("at", ["first", "middle", "last", "many"])
 @pytest.mark.parametrize("d,hq,tokens,many", [(64, 8, 1, False), (128, 8, 1, False), (256, 8, 1, False), (128, 16, 1, False), (64, 8, 4, False),
                                               (128, 8, 4, False), (256, 8, 2, False), (128, 8, 1, True), (64, 16, 1, True), (256, 8, 2, True)])
 def test_keys_far_below_one_that_dominates(d, hq, tokens, many, at):
@@ -454,12 +454,13 @@ def test_keys_far_below_one_that_dominates(d, hq, tokens, many, at):
     batch = 1300 if many else 600
     cache = H.make_cache(d, n // page + 5, 1, page, d)
     table = H.make_table(d, [n], page, cache.num_pages)
-    star = {"first": 0, "middle": 1501, "last": n - tokens}[at]
+    stars = {"first": [0], "middle": [1501], "last": [n - tokens], "many": list(range(7, n - tokens, 128 * 3))}[at]
     k, v = cache.k.view(torch.uint8), cache.v.view(torch.uint8)
     k[:, :, :, 0] = 0
-    k[table[0, star // page], 0, star % page] = 0
-    k[table[0, star // page], 0, star % page, 0] = 0x7E                        # 448
-    v[table[0, star // page], 0, star % page] = 0
+    for star in stars:
+        k[table[0, star // page], 0, star % page] = 0
+        k[table[0, star // page], 0, star % page, 0] = 0x7E                    # 448
+        v[table[0, star // page], 0, star % page] = 0
     cache.k_scale.fill_(2.0 ** -8)
     q = torch.randn(tokens, hq, d, generator=torch.Generator().manual_seed(d))
     gap = torch.tensor([0, 8, 12, 14, 17, 21, 30, 60.0])[torch.arange(hq) % 8]
@@ -623,6 +624,24 @@ def test_gather(d, hkv, page):
             for x, r in ((k, rk), (v, rv)):
                 got = x[int(cu[b]):int(cu[b + 1]), h].float().cpu().numpy()
                 assert np.array_equal(got, r.astype(np.float32))          # power-of-two scales: exact
+    assert (k[int(cu[-1]):] == 7).all() and (v[int(cu[-1]):] == 7).all()
+
+
+@pytest.mark.parametrize("page,d", [(16, 64), (64, 128)])
+def test_gather_writes_zeros_past_the_tables_capacity(page, d):
+    cache = H.make_cache(d, 6, 2, page, d)
+    table = np.array([[0, 1], [2, 3], [4, 5]], np.int32)
+    lens = [2 * page + 9, 5, 3 * page]                                    # a row of the table holds 2 pages
+    cu = H.cu_of(lens)
+    k, v = (torch.full((int(cu[-1]) + 3, 2, d), 7.0, dtype=bf16, device="cuda") for _ in range(2))
+    M.attn_kv8_gather(cache, H.i32(table), H.i32(cu), k, v)
+    keys = H.Keys(cache)
+    for b, n in enumerate(lens):
+        held = min(n, 2 * page)
+        for h in range(2):
+            for x, r in zip((k, v), keys.of(table[b], held, h)):
+                got = x[int(cu[b]):int(cu[b + 1]), h].float().cpu().numpy()
+                assert np.array_equal(got[:held], r.astype(np.float32)) and (got[held:] == 0).all()
     assert (k[int(cu[-1]):] == 7).all() and (v[int(cu[-1]):] == 7).all()
 
 
