@@ -29,6 +29,7 @@ a GPU.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -180,6 +181,17 @@ def _stream(stream) -> Optional[int]:
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda device: torch.cuda.current_stream(device).cuda_stream)
     return _raw_stream(torch.cuda.current_device())
+
+
+def _allocating_on(stream, like):
+    """The context in which results of a call on ``stream`` (None: the current one; a torch stream or a raw handle) are
+    allocated. A block of the current stream's pool may still be in use there, which ``stream`` does not wait for."""
+    if stream is None or not like.is_cuda:
+        return contextlib.nullcontext()
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=like.device)
+    return torch.cuda.stream(stream)
 
 
 class _Marshal:

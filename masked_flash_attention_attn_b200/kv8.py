@@ -29,7 +29,7 @@ from __future__ import annotations
 import ctypes
 import struct
 
-from . import MASK_KIND, _check, lib
+from . import MASK_KIND, _allocating_on, _check, lib
 
 PAGE_SIZES = (16, 32, 64, 128)
 
@@ -371,9 +371,11 @@ def attn_kv8_select(plan: Kv8Plan, cache: Kv8Cache, q, page_table, kv_lens, scor
 
 
 def forward_kv8(plan: Kv8Plan, cache: Kv8Cache, q, page_table, kv_lens, cu_seqlens_q=None, selected=None, stream=None):
-    """Allocate out / lse with torch and run attn_kv8_fwd (convenience)."""
+    """Allocate out / lse with torch and run attn_kv8_fwd (convenience). With ``stream`` (a torch stream or a raw
+    handle) they are allocated on it, like the results of an operation under torch.cuda.stream(stream)."""
     _shape(q, "q", 3)
-    out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty(q.shape[0], plan.hq, dtype=torch.float32, device=q.device)
+    with _allocating_on(stream, q):
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        lse = torch.empty(q.shape[0], plan.hq, dtype=torch.float32, device=q.device)
     attn_kv8_fwd(plan, cache, q, page_table, kv_lens, out, lse, cu_seqlens_q=cu_seqlens_q, selected=selected, stream=stream)
     return out, lse

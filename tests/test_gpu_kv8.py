@@ -911,6 +911,27 @@ def test_two_captured_graphs_of_two_plans_and_eager_calls_between():
     assert all(torch.equal(o, out) for o in outs)
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_results_of_a_call_on_another_stream_are_of_its_pool(raw):
+    lens = [900] * 40
+    cache, table, q, out, lse, plan = attend(42, lens, [1] * 40, hq=32, hkv=8, d=128, page=16, sample=10)
+    t, n = H.i32(table), H.i32(lens)
+    s = torch.cuda.Stream()
+    for _ in range(2):
+        torch.cuda.synchronize()
+        x, y = torch.empty_like(out), torch.empty_like(lse)
+        at = {x.data_ptr(), y.data_ptr()}
+        torch.cuda._sleep(10_000_000)
+        x.fill_(3)                               # still to come on the current stream when its block is free again
+        y.fill_(3)
+        del x, y
+        a, b = M.forward_kv8(plan, cache, q, t, n, stream=s.cuda_stream if raw else s)
+        assert not at & {a.data_ptr(), b.data_ptr()}
+        torch.cuda.synchronize()
+        assert torch.equal(a, out) and torch.equal(b, lse)
+        del a, b
+
+
 def test_two_plans_on_two_streams():
     lens = [9000, 20]
     cache, table, q, out, lse, _ = attend(40, lens, [1, 1], hq=8, hkv=2, d=128, page=16, sample=10)

@@ -170,6 +170,26 @@ def test_fwd_and_select_checks():
         M.attn_kv8_fwd(p, c, q, table, lens, out)
 
 
+def test_forward_kv8_allocates_on_its_stream(monkeypatch):
+    # the results of a call on another stream come from that stream's pool
+    inside, on, sizes = [], [], []
+
+    class Context:
+        def __enter__(self):
+            inside.append(True)
+
+        def __exit__(self, *_):
+            inside.pop()
+    empty = torch.empty
+    monkeypatch.setattr(kv8, "_allocating_on", lambda stream, like: on.append((stream, like)) or Context())
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: sizes.append(bool(inside)) or empty(*a, **k))
+    monkeypatch.setattr(kv8, "attn_kv8_fwd", lambda *a, **k: on.append(k["stream"]))
+    q = torch.zeros(3, 4, 64, dtype=bf16)
+    kv8._init()
+    out, lse = M.forward_kv8(cpu_plan(), cpu_cache(), q, None, None, stream=1234)
+    assert on == [(1234, q), 1234] and sizes == [True, True] and out.shape == q.shape and lse.shape == (3, 4)
+
+
 def test_gather_and_tables_checks():
     c = cpu_cache()
     k, table, cu = torch.zeros(9, 2, 64, dtype=bf16), torch.zeros(2, 5, dtype=i32), torch.zeros(3, dtype=i32)
