@@ -551,20 +551,22 @@ def attn_status_string(status: int) -> str:
 
 
 def forward(plan: Plan, q, k, v, stream=None):
-    """Allocate out / lse with torch and run attn_masked_fwd (convenience)."""
+    """Allocate out / lse with torch, on ``stream`` if one is given, and run attn_masked_fwd (convenience)."""
     import torch
-    out = torch.empty(q.shape[0], plan.hq, plan.head_dim, dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty(q.shape[0], plan.hq, dtype=torch.float32, device=q.device)
+    with _allocating_on(stream, q):
+        out = torch.empty(q.shape[0], plan.hq, plan.head_dim, dtype=torch.bfloat16, device=q.device)
+        lse = torch.empty(q.shape[0], plan.hq, dtype=torch.float32, device=q.device)
     attn_masked_fwd(plan, q, k, v, out, lse, stream)
     return out, lse
 
 
 def backward(plan: Plan, q, k, v, out, lse, dout, stream=None, dlse=None):
-    """Allocate dq / dk / dv with torch and run attn_masked_bwd (convenience)."""
+    """Allocate dq / dk / dv with torch, on ``stream`` if one is given, and run attn_masked_bwd (convenience)."""
     import torch
-    dq = torch.empty_like(q)
-    dk = torch.empty_like(k)
-    dv = torch.empty_like(v)
+    with _allocating_on(stream, q):
+        dq = torch.empty_like(q)
+        dk = torch.empty_like(k)
+        dv = torch.empty_like(v)
     attn_masked_bwd(plan, q, k, v, out, lse, dout, dq, dk, dv, stream, dlse=dlse)
     return dq, dk, dv
 

@@ -148,3 +148,25 @@ def test_device_mask_bits_checked():
         M.attn_plan(mask=W.MaskSpec("CUSTOM", bits=torch.zeros(80, dtype=torch.int64), word_offsets=off), **kw)
     with pytest.raises(ValueError, match="CUDA"):
         M.attn_plan(mask=W.MaskSpec("CUSTOM", bits=torch.zeros(80, dtype=torch.int32), word_offsets=off), **kw)
+
+
+def test_forward_and_backward_allocate_on_their_stream(monkeypatch):
+    # the results of a call on another stream come from that stream's pool
+    inside, on, made = [], [], []
+
+    class Context:
+        def __enter__(self):
+            inside.append(True)
+
+        def __exit__(self, *_):
+            inside.pop()
+    monkeypatch.setattr(M, "_allocating_on", lambda stream, like: on.append(stream) or Context())
+    for name in ("empty", "empty_like"):
+        real = getattr(torch, name)
+        monkeypatch.setattr(torch, name, lambda *a, _real=real, **k: made.append(bool(inside)) or _real(*a, **k))
+    monkeypatch.setattr(M, "attn_masked_fwd", lambda *a: on.append(a[-1]))
+    monkeypatch.setattr(M, "attn_masked_bwd", lambda *a, **k: on.append(a[-1]))
+    g = _good()
+    M.forward(_plan(), g["q"], g["k"], g["v"], stream=1234)
+    M.backward(_plan(), g["q"], g["k"], g["v"], g["out"], g["lse"], g["out"], stream=1234)
+    assert on == [1234] * 4 and made == [True] * 5
