@@ -107,7 +107,7 @@ attn_status_t attn_page_tables(const attn_page_tables_t* tables, attn_stream_t s
  * (exact for powers of two, but for subnormal codes). k_bounds is kept up in the same way.
  * A NaN among the new values makes the scale NaN until place 0 of the page is written again;
  * other pages, heads and (K or V) are not touched by it.
- * Errors: INVALID_ARG, UNSUPPORTED (page_size, head_dim), CUDA. */
+ * Errors: INVALID_ARG (also: k and v, or their scales, overlap), UNSUPPORTED (page_size, head_dim), CUDA. */
 attn_status_t attn_kv8_append(const attn_kv8_cache_t* cache, const void* k_new, int64_t k_stride, const void* v_new,
                               int64_t v_stride, const int32_t* slots, int32_t num_tokens, attn_stream_t stream);
 
@@ -117,7 +117,7 @@ attn_status_t attn_kv8_append(const attn_kv8_cache_t* cache, const void* k_new, 
  * cu_seqlens_k: DEVICE int32 [batch + 1], non-decreasing from 0; rows from cu_seqlens_k[batch] on
  * are left as they were. page_table: DEVICE int32 [batch][max_pages_per_seq]; tokens past its
  * max_pages_per_seq pages are zeros, as those of pages outside the cache.
- * Errors: INVALID_ARG, UNSUPPORTED (page_size, head_dim), CUDA. */
+ * Errors: INVALID_ARG (also: k_out and v_out overlap), UNSUPPORTED (page_size, head_dim), CUDA. */
 attn_status_t attn_kv8_gather(const attn_kv8_cache_t* cache, const int32_t* page_table, int32_t max_pages_per_seq,
                               const int32_t* cu_seqlens_k, int32_t batch, int64_t total_k, void* k_out, void* v_out,
                               attn_stream_t stream);
@@ -166,7 +166,7 @@ typedef struct {
  * 65 nats below the row's maximum. Results do not depend on timing (partial results are
  * joined in a fixed order).
  * Errors: INVALID_ARG (also: another device is current than the plan's, a cache of another shape
- * than the plan's), CUDA. */
+ * than the plan's, out overlaps q or lse), CUDA. */
 attn_status_t attn_kv8_fwd(const attn_kv8_plan_t* plan, const attn_kv8_cache_t* cache, const attn_kv8_batch_t* batch,
                            const int32_t* selected, int32_t n_selected, void* out, float* lse, attn_stream_t stream);
 
@@ -181,7 +181,8 @@ attn_status_t attn_kv8_fwd(const attn_kv8_plan_t* plan, const attn_kv8_cache_t* 
  * page, and a page whose scale is NaN has the largest finite score. scores (fp32 [total_q][hkv][max_pages_per_seq]) receives the scores of the pages a token
  * sees; its other entries are left as they were. The plan's mask must be CAUSAL (or FULL: each
  * token then sees all kv_len tokens). 0 <= sink, 1 <= recent, sink + recent <= n_selected.
- * Errors: INVALID_ARG, UNSUPPORTED (SLIDING_WINDOW plan), CUDA. */
+ * Errors: INVALID_ARG (also: scores and selected overlap), UNSUPPORTED (a SLIDING_WINDOW plan, more than 64 query
+ * heads per KV head), CUDA. */
 attn_status_t attn_kv8_select(const attn_kv8_plan_t* plan, const attn_kv8_cache_t* cache, const attn_kv8_batch_t* batch,
                               int32_t sink, int32_t recent, float* scores, int32_t* selected, int32_t n_selected,
                               attn_stream_t stream);

@@ -938,6 +938,8 @@ attn_status_t attn_kv8_append(const attn_kv8_cache_t* c, const void* k_new, int6
   if (!k_new || !v_new || !slots || misaligned(k_new, 16) || misaligned(v_new, 16) || misaligned(slots, 4))
     return ATTN_ERR_INVALID_ARG;
   if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8) return ATTN_ERR_INVALID_ARG;
+  const int64_t blocks = int64_t(c->num_pages) * c->hkv, codes = blocks * c->page_size * c->head_dim;
+  if (overlap(c->k, codes, c->v, codes) || overlap(c->k_scale, blocks * 4, c->v_scale, blocks * 4)) return ATTN_ERR_INVALID_ARG;
   AppendArgs a{};
   a.x[0] = static_cast<const __nv_bfloat16*>(k_new);
   a.x[1] = static_cast<const __nv_bfloat16*>(v_new);
@@ -980,6 +982,8 @@ attn_status_t attn_kv8_gather(const attn_kv8_cache_t* c, const int32_t* page_tab
   if (!page_table || !cu_seqlens_k || !k_out || !v_out || total_k >= (int64_t(1) << 31)) return ATTN_ERR_INVALID_ARG;
   if (misaligned(k_out, 16) || misaligned(v_out, 16) || misaligned(page_table, 4) || misaligned(cu_seqlens_k, 4))
     return ATTN_ERR_INVALID_ARG;
+  const int64_t bytes = total_k * c->hkv * c->head_dim * 2;
+  if (overlap(k_out, bytes, v_out, bytes)) return ATTN_ERR_INVALID_ARG;
   GatherArgs a{};
   a.codes[0] = static_cast<const uint8_t*>(c->k);
   a.codes[1] = static_cast<const uint8_t*>(c->v);
@@ -1012,6 +1016,7 @@ attn_status_t attn_kv8_select(const attn_kv8_plan_t* p, const attn_kv8_cache_t* 
   const int64_t rows = int64_t(b->total_q) * p->hkv;
   const int64_t chunks = (int64_t(b->max_pages_per_seq) + kScorePages - 1) / kScorePages;
   if (rows >= (int64_t(1) << 31) || chunks > 65535) return ATTN_ERR_INVALID_ARG;
+  if (overlap(scores, rows * b->max_pages_per_seq * 4, selected, rows * n_selected * 4)) return ATTN_ERR_INVALID_ARG;
   SelectArgs a{};
   a.b = batch_of(p, b);
   a.q = static_cast<const __nv_bfloat16*>(b->q);

@@ -876,6 +876,7 @@ attn_status_t attn_kv8_fwd(const attn_kv8_plan_t* p, const attn_kv8_cache_t* c, 
   if (!out || misaligned(out, 16) || misaligned(lse, 4)) return ATTN_ERR_INVALID_ARG;
   const int64_t row = int64_t(p->hq) * p->d;
   if (overlap(b->q, (int64_t(b->total_q - 1) * b->q_stride + row) * 2, out, int64_t(b->total_q) * row * 2)) return ATTN_ERR_INVALID_ARG;
+  if (overlap(out, int64_t(b->total_q) * row * 2, lse, int64_t(b->total_q) * p->hq * 4)) return ATTN_ERR_INVALID_ARG;
   FwdArgs a{};
   a.b = batch_of(p, b);
   a.q = static_cast<const __nv_bfloat16*>(b->q);

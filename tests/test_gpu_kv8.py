@@ -429,6 +429,27 @@ def test_calls_that_are_refused():
         M.attn_kv8_fwd(plan, cache, q, table, lens, torch.empty_like(q))
 
 
+def test_outputs_that_overlap_are_refused():
+    cache = H.make_cache(1, 8, 2, 16, 64)
+    plan = M.attn_kv8_plan(hq=4, hkv=2, head_dim=64, page_size=16, mask=masks.causal())
+    q = torch.zeros(2, 4, 64, dtype=bf16, device="cuda")
+    table, lens = H.i32([[0, 1], [2, 3]]), H.i32([20, 9])
+    out = torch.zeros_like(q)
+    for at in (0, 256 - 8):                      # out is 256 words
+        with pytest.raises(M.AttnError, match="INVALID"):
+            M.attn_kv8_fwd(plan, cache, q, table, lens, out, out.view(-1).view(torch.float32)[at:at + 8].view(2, 4))
+    both = torch.zeros(2, 2, 2, device="cuda")
+    with pytest.raises(M.AttnError, match="INVALID"):
+        M.attn_kv8_select(plan, cache, q, table, lens, both, both.view(torch.int32))
+    k = torch.zeros(29, 2, 64, dtype=bf16, device="cuda")
+    with pytest.raises(M.AttnError, match="INVALID"):
+        M.attn_kv8_gather(cache, table, H.i32([0, 20, 29]), k, k)
+    shared = M.Kv8Cache.wrap(cache.k, cache.k, cache.k_scale, cache.v_scale)
+    with pytest.raises(M.AttnError, match="INVALID"):
+        M.attn_kv8_append(shared, k, k, H.i32(np.arange(29)))
+    M.attn_kv8_fwd(plan, shared, q, table, lens, out)      # only read: keys that are the values too are fine
+
+
 def test_scores_that_rise_along_the_keys_and_wide_scales():
     # every step raises the running maximum; the scales of the pages differ by 2^40
     page, d = 16, 128

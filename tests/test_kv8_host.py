@@ -241,6 +241,18 @@ def test_c_append_and_gather_refusals(attn_lib):
     assert g(None, 2, None, 0, 0, None, None) == 0
 
 
+def test_c_refuses_outputs_that_overlap(attn_lib):
+    # 4 pages x 2 heads x 16 x 64: 8192 bytes of codes, 32 of scales; 5 rows x 2 x 64 bf16: 1280 bytes
+    L = attn_lib.lib()
+    app = lambda **kw: L.attn_kv8_append(ctypes.byref(c_cache(**kw)), 1 << 20, 128, 1 << 21, 128, 1 << 22, 3, None)  # noqa: E731
+    apart = dict(k=0x10000, v=0x20000, k_scale=0x30000, v_scale=0x40000)
+    for kw in (dict(v=0x10000), dict(v=0x10000 + 8192 - 16), dict(v=0x10000 - 8192 + 16), dict(v_scale=0x30000), dict(v_scale=0x30000 + 28)):
+        assert app(**{**apart, **kw}) == INVALID, kw
+    c = c_cache(**apart)
+    for k, v in ((0x50000, 0x50000), (0x50000, 0x50000 + 1280 - 16), (0x50000, 0x50000 - 1280 + 16)):
+        assert L.attn_kv8_gather(ctypes.byref(c), 0x60000, 2, 0x70000, 1, 5, k, v, None) == INVALID
+
+
 def test_c_plan_refusals(attn_lib):
     L = attn_lib.lib()
     h = ctypes.c_void_p()
