@@ -145,6 +145,14 @@ def _rows(t, name, heads, head_dim, dev):
     return t.data_ptr(), s0, n
 
 
+def _int32(x, name):
+    """``x`` as an int of 32 bits (ctypes would drop the bits above)."""
+    n = int(x)
+    if not -1 << 31 <= n < 1 << 31:
+        raise ValueError(f"{name} = {n} does not fit in 32 bits")
+    return n
+
+
 def _on_current(dev, stream):
     """The raw stream of a call whose tensors are on device ``dev``."""
     if dev < 0:
@@ -243,6 +251,8 @@ def attn_page_tables(*, page_table, old_lens, new_lens, free_pages, free_state, 
                ((batch, width), lens, lens, (pages,), four, four, lens, (batch + 1,), (tokens,), (tokens,)), dev)
     if positions is None:
         at[9] = 0
+    if page_size not in PAGE_SIZES:
+        page_size = _int32(page_size, "page_size")       # the library's to refuse
     a = _TABLES(batch, width, pages, page_size, tokens, *at)
     st = lib().attn_page_tables(a, _on_current(dev, stream))
     if st:
@@ -293,8 +303,9 @@ def attn_kv8_plan(*, hq: int, hkv: int, head_dim: int, page_size: int, mask, sca
     masks.causal(), masks.full() or masks.sliding_window(w); ``max_q_len``: query tokens per request that
     are common."""
     _init()
-    p = attn_kv8_problem_t(int(hq), int(hkv), int(head_dim), int(page_size), float(scale), MASK_KIND[mask.kind],
-                           int(getattr(mask, "window", 0) or 0), int(max_q_len))
+    p = attn_kv8_problem_t(_int32(hq, "hq"), _int32(hkv, "hkv"), _int32(head_dim, "head_dim"), _int32(page_size, "page_size"),
+                           float(scale), MASK_KIND[mask.kind], _int32(getattr(mask, "window", 0) or 0, "window"),
+                           _int32(max_q_len, "max_q_len"))
     h = ctypes.c_void_p()
     _check(lib().attn_kv8_plan(ctypes.byref(p), ctypes.byref(h)), "attn_kv8_plan")
     return Kv8Plan(h.value, p.hq, p.hkv, p.head_dim, p.page_size, torch.cuda.current_device())
@@ -364,7 +375,7 @@ def attn_kv8_select(plan: Kv8Plan, cache: Kv8Cache, q, page_table, kv_lens, scor
     n = _shape(selected, "selected", 3)[2]
     cp = _ptr(scores, "scores", _F32, (total, plan.hkv, width), dev)
     sp = _ptr(selected, "selected", _I32, (total, plan.hkv, n), dev)
-    st = lib().attn_kv8_select(plan.handle, cache._ref, b, int(sink), int(recent), cp, sp, n,
+    st = lib().attn_kv8_select(plan.handle, cache._ref, b, _int32(sink, "sink"), _int32(recent, "recent"), cp, sp, n,
                                _on_current(dev, stream))
     if st:
         _check(st, "attn_kv8_select")

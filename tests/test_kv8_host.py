@@ -212,6 +212,26 @@ def test_gather_and_tables_checks():
             M.attn_page_tables(**dict(good, **{name: bad}))
 
 
+def test_integers_past_32_bits_are_refused():
+    # their low 32 bits would be taken: a window of 2^32 + 5 for one of 5
+    good = dict(hq=4, hkv=2, head_dim=64, page_size=16, mask=masks.causal(), max_q_len=1)
+    for name in ("hq", "hkv", "head_dim", "page_size", "max_q_len"):
+        with pytest.raises(ValueError, match=name):
+            M.attn_kv8_plan(**dict(good, **{name: (1 << 32) + good[name]}))
+    with pytest.raises(ValueError, match="window"):
+        M.attn_kv8_plan(**dict(good, mask=masks.sliding_window((1 << 32) + 5)))
+    c, p = cpu_cache(), cpu_plan()
+    q, table, lens = torch.zeros(3, 4, 64, dtype=bf16), torch.zeros(3, 5, dtype=i32), torch.zeros(3, dtype=i32)
+    sc, sel = torch.zeros(3, 2, 5), torch.zeros(3, 2, 4, dtype=i32)
+    for kw in (dict(sink=1 << 32), dict(recent=(1 << 32) + 1)):
+        with pytest.raises(ValueError, match="32 bits"):
+            M.attn_kv8_select(p, c, q, table, lens, sc, sel, **kw)
+    z = lambda *s: torch.zeros(*s, dtype=i32)  # noqa: E731
+    with pytest.raises(ValueError, match="page_size"):
+        M.attn_page_tables(page_table=z(3, 4), old_lens=z(3), new_lens=z(3), free_pages=z(8), free_state=z(4), page_size=(1 << 32) + 16,
+                           next_state=z(4), kv_lens=z(3), cu_seqlens_q=z(4), slots=z(6))
+
+
 # ---- the C ABI's refusals (no GPU: every one comes before a CUDA call) ------------------------------
 INVALID, UNSUPPORTED = 1, 2
 
