@@ -63,7 +63,8 @@ typedef struct {
  *               in order and their pages in order; the tokens old .. new - 1 get slots
  *   new < old   (finished: new = 0; rejected draft tokens) the pages past the new length go to
  *               the ring's tail in the same order; its table entries stay as they were
- * Pages given back in a call are not taken again by the same call.
+ * Pages given back in a call are not taken again by the same call. A page belongs to one request: pages are not
+ * counted, and one in the rows of two requests (a shared prefix) would go to the ring twice, without a status.
  * Nobody grows (kv_lens = min(old, new), no slots) when the step cannot be done: status 2, a
  * new length is negative or above max_pages_per_seq * page_size (that request stays at its old
  * length); else 3, more new tokens than max_tokens; else 1, too few free pages. Requests that
@@ -137,7 +138,8 @@ typedef struct {
 
 /* Make a plan for the current device: the kernel's shape and a workspace for the partial
  * results of requests whose keys several CTAs share (at most 40 MiB). Calls on one plan must be
- * ordered one after another (one stream, or events); streams that overlap need a plan each.
+ * ordered one after another (one stream, or events); streams that overlap need a plan each. A captured
+ * graph reads the plan's workspace at every replay: destroy the plan after the graphs that hold its calls.
  * Errors: INVALID_ARG, UNSUPPORTED, OOM, CUDA. */
 attn_status_t attn_kv8_plan(const attn_kv8_problem_t* problem, attn_kv8_plan_t** out_plan);
 attn_status_t attn_kv8_plan_destroy(attn_kv8_plan_t* plan);

@@ -87,11 +87,17 @@ struct FwdArgs {
 
 // A CTA of W warps. Merging the warps and starting on the next item cost about as many instructions as
 // 27 steps in a CTA of 8 warps, in proportion less in one of 2; many warps leave fewer parts of few
-// long items to join. Both sides measured at d = 128, 8 KV heads, 32 query heads, 250-400 MB of codes:
-//   512 items of 2-4 K keys:    75.3 us with 8 warps, 80.5 with 2
-//   1024 items of 1-2 K keys:   80.6, 79.0
-//   8192 items of 150-300 keys: 178,  127
-// so CTAs of 2 warps from kManyItems items on (requests, or tokens with selected pages, times KV heads).
+// long items to join. So CTAs of 2 warps from kManyItems items on (requests, or tokens with selected pages, times
+// KV heads); the lengths are on the device, so the rule cannot see them. us with 8 (d = 256, or more than 8 rows: 4) warps
+// and with 2, 8 KV heads, requests x keys:
+//                          512 items   1200 items              2400 items    4800 items   8192 items
+//                          2-4 K keys  8-16 K       2-4 K      1-2 K         300-600      150-300
+//   d = 128,  4 rows       75 / 81     602 / 621    172 / 182  178 / 196     154 / 131    187 / 133
+//   d =  64,  4 rows                   336 / 336    109 / 103  125 / 111     119 /  87    151 /  98
+//   d = 256,  2 rows                  1150 / 1133   304 / 315  303 / 317     223 / 214    246 / 205
+//   d = 128, 16 rows                   705 / 692    211 / 201  234 / 216     213 / 178    259 / 201
+//   d = 256,  8 rows                  1169 / 1174   317 / 328  312 / 320     244 / 223    279 / 229
+// Many long items lose up to a tenth by it, short ones gain up to a third.
 constexpr int kManyItems = 1200;
 
 template <int D, int NG, int W>

@@ -215,7 +215,8 @@ class Kv8Cache:
 
 
 class Kv8Plan:
-    """Owns an attn_kv8_plan_t. Calls on one plan must be ordered one after another."""
+    """Owns an attn_kv8_plan_t. Calls on one plan must be ordered one after another, and a plan must live as long as a
+    captured graph that holds its calls is replayed (its workspace is freed with it)."""
 
     def __init__(self, handle, hq, hkv, head_dim, page_size, index):
         self.handle, self.hq, self.hkv, self.head_dim, self.page_size, self.index = handle, hq, hkv, head_dim, page_size, index

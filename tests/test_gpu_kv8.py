@@ -648,6 +648,18 @@ def test_gather(d, hkv, page):
     assert (k[int(cu[-1]):] == 7).all() and (v[int(cu[-1]):] == 7).all()
 
 
+def check_gathered(cache, table, lens):
+    """The requests' cached tokens, gathered, against the oracle's values (power-of-two scales: exact)."""
+    cu = H.cu_of(lens)
+    k, v = (torch.empty(int(cu[-1]), cache.hkv, cache.head_dim, dtype=bf16, device="cuda") for _ in range(2))
+    M.attn_kv8_gather(cache, H.i32(table), H.i32(cu), k, v)
+    keys = H.Keys(cache)
+    for b, n in enumerate(lens):
+        for h in range(cache.hkv):
+            for x, r in zip((k, v), keys.of(table[b], int(n), h)):
+                assert np.array_equal(x[int(cu[b]):int(cu[b + 1]), h].float().cpu().numpy(), r.astype(np.float32))
+
+
 @pytest.mark.parametrize("page,d", [(16, 64), (64, 128)])
 def test_gather_writes_zeros_past_the_tables_capacity(page, d):
     cache = H.make_cache(d, 6, 2, page, d)
