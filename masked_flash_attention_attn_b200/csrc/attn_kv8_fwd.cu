@@ -61,7 +61,8 @@ constexpr float kNone = -3.402823466e38f;  // reference of a row that has seen n
 // largest of its 16 keys, however far those are below the row's maximum. (With the running maximum as reference,
 // keys 17 nats below a sink lost a third of their sum.) Downwards until the row's sum is 2^kGrow, far from the
 // end of fp32 for the products too: keys up to 65 nats below the maximum.
-// (16 verifications at d = 256: 47.1 us with the maximum as reference, 48.3 so; decode steps within 1 %.)
+// (With the maximum as reference / so: 32 x 2-4 K keys at d = 128 with 4 rows 42.3 / 42.4 us, 16 rows 50.9 / 52.7,
+// 32 rows 76.8 / 79.3; 16 verifications at d = 256 46.5 / 46.9. Both ends in one compare of |x - m|: two compares 1-2 % more.)
 constexpr float kHead = 6.f;
 constexpr float kRange = 14.f;
 constexpr int kGrow = 80;
@@ -89,15 +90,16 @@ struct FwdArgs {
 // 27 steps in a CTA of 8 warps, in proportion less in one of 2; many warps leave fewer parts of few
 // long items to join. So CTAs of 2 warps from kManyItems items on (requests, or tokens with selected pages, times
 // KV heads); the lengths are on the device, so the rule cannot see them. us with 8 (d = 256, or more than 8 rows: 4) warps
-// and with 2, 8 KV heads, requests x keys:
-//                          512 items   1200 items              2400 items    4800 items   8192 items
-//                          2-4 K keys  8-16 K       2-4 K      1-2 K         300-600      150-300
-//   d = 128,  4 rows       75 / 81     602 / 621    172 / 182  178 / 196     154 / 131    187 / 133
-//   d =  64,  4 rows                   336 / 336    109 / 103  125 / 111     119 /  87    151 /  98
-//   d = 256,  2 rows                  1150 / 1133   304 / 315  303 / 317     223 / 214    246 / 205
-//   d = 128, 16 rows                   705 / 692    211 / 201  234 / 216     213 / 178    259 / 201
-//   d = 256,  8 rows                  1169 / 1174   317 / 328  312 / 320     244 / 223    279 / 229
-// Many long items lose up to a tenth by it, short ones gain up to a third.
+// / with 2, 8 KV heads, requests x keys:
+//                    64 x 2-4 K  150 x 8-16 K  150 x 2-4 K  300 x 1-2 K  600 x 300-600  1024 x 150-300
+//   d = 128,  4 rows   92 /  98   586 /  616    170 / 184    177 / 184     154 / 133      186 / 133
+//   d =  64,  4 rows   56 /  54   330 /  328    109 / 104    123 / 108     120 /  88      150 /  98
+//   d = 256,  2 rows  161 / 158  1153 / 1157    315 / 317    309 / 317     223 / 209      250 / 205
+//   d = 128, 16 rows  102 / 100   653 /  633    203 / 193    225 / 208     208 / 175      260 / 203
+//   d = 128, 32 rows  150 / 152  1043 / 1061    315 / 311    360 / 347     343 / 307      431 / 367
+//   d = 256,  8 rows  158 / 174  1153 / 1159    320 / 326    326 / 328     246 / 225      283 / 229
+//   d =  64, 32 rows  106 / 100   719 /  705    227 / 214    250 / 225     246 / 205      319 / 238
+// Many long items lose up to 8 % by it (decode at d = 128), short ones gain up to a third.
 constexpr int kManyItems = 1200;
 
 template <int D, int NG, int W>
@@ -537,7 +539,7 @@ __global__ void __launch_bounds__(32 * W, Cfg<D, NG, W>::CTAS) kv8_fwd_kernel(Fw
             if (key + g + 8 >= hi || key + g + 8 < lo) s[n][c + 2] = -INFINITY;
           }
         }
-        out_of_range |= fabsf(fmaxf(s[n][0], s[n][2]) - m[n][0]) > kRange || fabsf(fmaxf(s[n][1], s[n][3]) - m[n][1]) > kRange;
+        out_of_range |= (fabsf(fmaxf(s[n][0], s[n][2]) - m[n][0]) > kRange) | (fabsf(fmaxf(s[n][1], s[n][3]) - m[n][1]) > kRange);
       }
       if (__any_sync(~0u, out_of_range)) {        // move the references and rescale
 #pragma unroll
